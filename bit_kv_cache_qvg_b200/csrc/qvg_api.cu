@@ -215,12 +215,14 @@ qvg_status cuda_status(cudaError_t e) { return e == cudaSuccess ? QVG_OK : QVG_E
 // kernel from CUDA events recorded on the launching stream around each launch.
 enum Kind {
   K_DEQUANT, K_RESIDUAL, K_RESIDUAL_QUANT, K_ROWNORM, K_INIT, K_ASSIGN_EXACT, K_ASSIGN_TC,
-  K_RECHECK, K_UPD_BUCKET, K_UPD_SUM, K_UPD_CENT, K_ATTN, K_ROPE, K_STAT, K_NKINDS
+  K_RECHECK, K_UPD_BUCKET, K_UPD_SUM, K_UPD_CENT, K_ATTN, K_ROPE, K_STAT,
+  K_BATCH, K_WEIGHTS, K_EVICT, K_NKINDS
 };
 const char* const kKindNames[K_NKINDS] = {
   "qvg_dequant_fused", "qvg_residual", "qvg_residual_quant", "qvg_row_norms", "qvg_init_centroids",
   "qvg_assign_exact", "qvg_kmeans_assign", "qvg_assign_recheck", "qvg_update_bucket", "qvg_update_sum",
-  "qvg_update_centroids", "qvg_attention_fused", "qvg_rope_tables", "qvg_range_stat"};
+  "qvg_update_centroids", "qvg_attention_fused", "qvg_rope_tables", "qvg_range_stat",
+  "qvg_attention_batch", "qvg_attention_weights", "qvg_evict"};
 
 struct Profiler {
   std::mutex mu;
@@ -602,6 +604,136 @@ qvg_status qvg_attention(const qvg_config* cfg, const qvg_packed* k, const qvg_p
   a.workspace = workspace;
   a.ws_bytes = workspace != nullptr ? ws_bytes : 0;
   st = cuda_status(plaunch(K_ATTN, s, [&] { return launch_attention(a, s); }));
+  if (st == QVG_OK && fault_injected("stream")) st = QVG_ERR_CUDA;
+  return st;
+}
+
+// Arguments that the two calls on a batch share; *max_pos gets the largest
+// position the tables cover.
+static qvg_status check_batch(const qvg_config* cfg, int64_t Nk, int32_t H, int32_t d, const qvg_batch* b) {
+  const qvg_status st = check_config(cfg, Nk, H, d, QVG_BF16);
+  if (st != QVG_OK) return st;
+  if (b == nullptr || Nk < 1 || b->B < 1 || b->group < 1 || b->Nq < 1 || b->Nt < 0 || (b->causal != 0 && b->causal != 1))
+    return QVG_ERR_INVALID_ARG;
+  const int64_t most = int64_t(1) << 23;
+  if (b->Nq >= most || b->Nt >= most || (int64_t)b->B * b->group >= most || (int64_t)b->B * b->group * b->Nq >= most ||
+      (int64_t)H * b->B >= most)
+    return QVG_ERR_UNSUPPORTED;
+  return QVG_OK;
+}
+
+static qvg_status check_packed(const qvg_config* cfg, const qvg_packed* p, size_t align_codes, bool tables) {
+  const bool sym = cfg->scale_mode == QVG_SCALE_SYM;
+  const size_t ng = (size_t)(kD / cfg->group_size);
+  if (p == nullptr || p->codes == nullptr || p->scale == nullptr || (p->zero == nullptr && !sym)) return QVG_ERR_INVALID_ARG;
+  if (cfg->T > 0 && p->assign == nullptr) return QVG_ERR_INVALID_ARG;
+  if (cfg->T > 0 && tables && (p->centroids == nullptr || !aligned(p->centroids, 16))) return QVG_ERR_INVALID_ARG;
+  if (!aligned(p->codes, align_codes) || !aligned(p->scale, ng) || (!sym && !aligned(p->zero, ng))) return QVG_ERR_INVALID_ARG;
+  return QVG_OK;
+}
+
+static qvg_status check_batch_pointers(const qvg_batch* b, int64_t Nk, bool values, const void* tables, size_t tables_bytes,
+                                       const void* workspace, int64_t* max_pos) {
+  if (b->Q == nullptr || b->q_pos == nullptr || !aligned(b->Q, 16) || !aligned(b->q_pos, 8) || !aligned(b->k_pos, 8))
+    return QVG_ERR_INVALID_ARG;
+  if (b->Nt > 0 && (b->tail_k == nullptr || !aligned(b->tail_k, 16) || !aligned(b->tail_pos, 8) || !aligned(b->tail_len, 4) ||
+                    (values && (b->tail_v == nullptr || !aligned(b->tail_v, 16)))))
+    return QVG_ERR_INVALID_ARG;
+  if (tables == nullptr || !aligned(tables, 16) || workspace == nullptr || !aligned(workspace, 16) ||
+      tables_bytes < kRopeHeaderBytes + kRopeRowBytes)
+    return QVG_ERR_INVALID_ARG;
+  *max_pos = std::min<int64_t>((int64_t)((tables_bytes - kRopeHeaderBytes) / kRopeRowBytes), kRopeMaxPositions) - 1;
+  if (b->k_pos == nullptr && Nk - 1 > *max_pos) return QVG_ERR_INVALID_ARG;   // the cache's positions must be covered
+  return QVG_OK;
+}
+
+static BatchArgs batch_args(const qvg_config* cfg, int64_t Nk, int32_t H, const qvg_batch* b) {
+  BatchArgs a{};
+  a.batch = b; a.Nk = Nk; a.H = H; a.K = cfg->K; a.T = cfg->T; a.G = cfg->group_size;
+  a.sym = cfg->scale_mode == QVG_SCALE_SYM ? 1 : 0;
+  return a;
+}
+
+size_t qvg_attention_batch_workspace_bytes(const qvg_config* cfg, int64_t Nk, int32_t H, const qvg_batch* batch) {
+  int dev = 0;
+  if (check_batch(cfg, Nk, H, kD, batch) != QVG_OK) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) { (void)cudaGetLastError(); return 0; }
+  return attention_batch_workspace_bytes(batch_args(cfg, Nk, H, batch));
+}
+
+size_t qvg_attention_weights_workspace_bytes(const qvg_config* cfg, int64_t Nk, int32_t H, const qvg_batch* batch) {
+  int dev = 0;
+  if (check_batch(cfg, Nk, H, kD, batch) != QVG_OK) return 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) { (void)cudaGetLastError(); return 0; }
+  return attention_weights_workspace_bytes(batch_args(cfg, Nk, H, batch));
+}
+
+qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* k, const qvg_packed* v, int64_t Nk, int32_t H,
+                               int32_t d, const qvg_batch* batch, const void* tables, size_t tables_bytes, void* O,
+                               void* workspace, size_t ws_bytes, qvg_stream_t stream_) {
+  qvg_status st = check_batch(cfg, Nk, H, d, batch);
+  if (st != QVG_OK) return st;
+  int64_t max_pos = 0;
+  if ((st = check_packed(cfg, k, 2, true)) != QVG_OK || (st = check_packed(cfg, v, 2, true)) != QVG_OK) return st;
+  if ((st = check_batch_pointers(batch, Nk, true, tables, tables_bytes, workspace, &max_pos)) != QVG_OK) return st;
+  if (O == nullptr || !aligned(O, 16)) return QVG_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  BatchArgs a = batch_args(cfg, Nk, H, batch);
+  a.k = k; a.v = v; a.tables = tables; a.max_pos = max_pos;
+  if (ws_bytes < attention_batch_workspace_bytes(a)) return QVG_ERR_WORKSPACE_TOO_SMALL;
+  st = peek_sticky(tables, s);
+  if (st != QVG_OK) return st;
+  st = cuda_status(plaunch(K_BATCH, s, [&] { return launch_attention_batch(a, O, workspace, s); }));
+  if (st == QVG_OK && fault_injected("stream")) st = QVG_ERR_CUDA;
+  return st;
+}
+
+qvg_status qvg_attention_weights(const qvg_config* cfg, const qvg_packed* k, int64_t Nk, int32_t H, int32_t d,
+                                 const qvg_batch* batch, const void* tables, size_t tables_bytes,
+                                 const float* received, float* out, void* workspace, size_t ws_bytes,
+                                 qvg_stream_t stream_) {
+  qvg_status st = check_batch(cfg, Nk, H, d, batch);
+  if (st != QVG_OK) return st;
+  int64_t max_pos = 0;
+  if ((st = check_packed(cfg, k, 2, true)) != QVG_OK) return st;
+  if ((st = check_batch_pointers(batch, Nk, false, tables, tables_bytes, workspace, &max_pos)) != QVG_OK) return st;
+  if (out == nullptr || !aligned(out, 4) || !aligned(received, 4)) return QVG_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  BatchArgs a = batch_args(cfg, Nk, H, batch);
+  a.k = k; a.tables = tables; a.max_pos = max_pos;
+  if (ws_bytes < attention_weights_workspace_bytes(a)) return QVG_ERR_WORKSPACE_TOO_SMALL;
+  st = peek_sticky(tables, s);
+  if (st != QVG_OK) return st;
+  st = cuda_status(plaunch(K_WEIGHTS, s, [&] { return launch_attention_weights(a, received, out, workspace, s); }));
+  if (st == QVG_OK && fault_injected("stream")) st = QVG_ERR_CUDA;
+  return st;
+}
+
+qvg_status qvg_evict(const qvg_config* cfg, const qvg_packed* k, const qvg_packed* v, int64_t Nk, int32_t H, int32_t d,
+                     const float* weights, const int64_t* k_pos, int64_t keep, int64_t first, int64_t recent,
+                     const qvg_packed* k_out, const qvg_packed* v_out, int32_t* kept, int64_t* pos_out,
+                     float* weights_out, qvg_stream_t stream_) {
+  qvg_status st = check_config(cfg, Nk, H, d, QVG_BF16);
+  if (st != QVG_OK) return st;
+  for (const qvg_packed* p : {k, v, k_out, v_out})
+    if ((st = check_packed(cfg, p, 16, false)) != QVG_OK) return st;
+  if (keep < 1 || keep > Nk || first < 0 || recent < 0 || first > keep || recent > keep - first || weights == nullptr ||
+      kept == nullptr || !aligned(weights, 4) || !aligned(kept, 4) || !aligned(k_pos, 8) || !aligned(pos_out, 8) ||
+      !aligned(weights_out, 4))
+    return QVG_ERR_INVALID_ARG;
+  for (const qvg_packed* in : {k, v})
+    for (const qvg_packed* out : {k_out, v_out})
+      if (in->codes == out->codes || in->scale == out->scale || (cfg->T > 0 && in->assign == out->assign) ||
+          (cfg->scale_mode == QVG_SCALE_ASYM && in->zero == out->zero))
+        return QVG_ERR_INVALID_ARG;
+  if (k_out->codes == v_out->codes || weights_out == weights || (pos_out != nullptr && pos_out == k_pos))
+    return QVG_ERR_INVALID_ARG;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  EvictArgs a{};
+  a.k = k; a.v = v; a.k_out = k_out; a.v_out = v_out; a.weights = weights; a.k_pos = k_pos; a.kept = kept;
+  a.pos_out = pos_out; a.weights_out = weights_out; a.Nk = Nk; a.keep = keep; a.first = first; a.recent = recent;
+  a.H = H; a.T = cfg->T; a.G = cfg->group_size; a.sym = cfg->scale_mode == QVG_SCALE_SYM ? 1 : 0;
+  st = cuda_status(plaunch(K_EVICT, s, [&] { return launch_evict(a, s); }));
   if (st == QVG_OK && fault_injected("stream")) st = QVG_ERR_CUDA;
   return st;
 }

@@ -181,4 +181,34 @@ int attention_split(int T, int64_t Nk, int64_t Nq, int H, int forced, size_t ws_
 size_t attention_workspace_bytes(int T, int64_t Nk, int64_t Nq, int H, int forced);
 size_t attention_smem_bytes();
 
+// ---- a batch over a shared prefix (kernel_attention_rows.cu)
+struct BatchArgs {
+  const qvg_packed* k;         // K cache: H blocks of Nk tokens (bf16 tables)
+  const qvg_packed* v;         // V cache, same configuration (null: weights)
+  const qvg_batch* batch;
+  const void* tables;          // rotary tables
+  int64_t max_pos;             // largest position the tables cover
+  int64_t Nk;
+  int H, K, T, G, sym;
+};
+// O [B][H * group][Nq][d] bf16.  ws: attention_batch_workspace_bytes.
+cudaError_t launch_attention_batch(const BatchArgs& a, void* O, void* ws, cudaStream_t s);
+size_t attention_batch_workspace_bytes(const BatchArgs& a);
+// out [H][Nk] = received (null: zeros) + the weights.  ws: attention_weights_workspace_bytes.
+cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, float* out, void* ws, cudaStream_t s);
+size_t attention_weights_workspace_bytes(const BatchArgs& a);
+
+// ---- eviction (kernels_evict.cu)
+struct EvictArgs {
+  const qvg_packed *k, *v, *k_out, *v_out;
+  const float* weights;        // [H][Nk]
+  const int64_t* k_pos;        // [H][Nk] or null
+  int32_t* kept;               // [H][keep]
+  int64_t* pos_out;            // [H][keep] or null
+  float* weights_out;          // [H][keep] or null
+  int64_t Nk, keep, first, recent;
+  int H, T, G, sym;
+};
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s);
+
 }  // namespace qvg

@@ -72,6 +72,12 @@ class _Packed(C.Structure):
                 ("assign", C.c_void_p), ("centroids", C.c_void_p)]
 
 
+class _Batch(C.Structure):
+    _fields_ = [("B", C.c_int32), ("group", C.c_int32), ("Nq", C.c_int64), ("Nt", C.c_int64), ("Q", C.c_void_p),
+                ("q_pos", C.c_void_p), ("k_pos", C.c_void_p), ("tail_k", C.c_void_p), ("tail_v", C.c_void_p),
+                ("tail_pos", C.c_void_p), ("tail_len", C.c_void_p), ("causal", C.c_int32)]
+
+
 _lib = None
 
 # Every exported symbol of include/qvg.h with its ctypes signature.
@@ -112,6 +118,18 @@ _SIGS = {
     "qvg_attention_set_split": (C.c_int32, [C.c_int32]),
     "qvg_attention_split": (C.c_int32, [C.POINTER(Config), C.c_int64, C.c_int32, C.c_int64, C.c_size_t]),
     "qvg_attention_workspace_bytes": (C.c_size_t, [C.POINTER(Config), C.c_int64, C.c_int32, C.c_int64]),
+    "qvg_attention_batch": (C.c_int, [C.POINTER(Config), C.POINTER(_Packed), C.POINTER(_Packed), C.c_int64, C.c_int32,
+                                      C.c_int32, C.POINTER(_Batch), C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p,
+                                      C.c_size_t, C.c_void_p]),
+    "qvg_attention_weights": (C.c_int, [C.POINTER(Config), C.POINTER(_Packed), C.c_int64, C.c_int32, C.c_int32,
+                                        C.POINTER(_Batch), C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p, C.c_void_p,
+                                        C.c_size_t, C.c_void_p]),
+    "qvg_attention_batch_workspace_bytes": (C.c_size_t, [C.POINTER(Config), C.c_int64, C.c_int32, C.POINTER(_Batch)]),
+    "qvg_attention_weights_workspace_bytes": (C.c_size_t, [C.POINTER(Config), C.c_int64, C.c_int32,
+                                                           C.POINTER(_Batch)]),
+    "qvg_evict": (C.c_int, [C.POINTER(Config), C.POINTER(_Packed), C.POINTER(_Packed), C.c_int64, C.c_int32, C.c_int32,
+                            C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int64, C.POINTER(_Packed),
+                            C.POINTER(_Packed), C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
     "qvg_profile_enable": (None, [C.c_int]),
     "qvg_profile_reset": (None, []),
     "qvg_profile_launches": (C.c_int64, []),
@@ -331,6 +349,199 @@ def attention_split(cfg: Config, Nk: int, H: int, Nq: int, ws_bytes: int = 0) ->
 def attention_workspace_bytes(cfg: Config, Nk: int, H: int, Nq: int) -> int:
     """qvg_attention_workspace_bytes: the workspace the preferred cut needs."""
     return int(lib().qvg_attention_workspace_bytes(C.byref(cfg), Nk, H, Nq))
+
+
+@dataclass
+class Tail:
+    """Each sequence's own newest tokens, not compressed (the tail of a qvg_batch):
+    k, v [B][H][Nt][d] bf16 (k before the rotary embedding; v is not read by
+    attention_weights), pos [B][Nt] int64 (None: Nk + i) and length [B] int32
+    (None: Nt), the tokens each tail holds."""
+    k: torch.Tensor
+    v: Optional[torch.Tensor] = None
+    pos: Optional[torch.Tensor] = None
+    length: Optional[torch.Tensor] = None
+
+
+def _device_tensor(t: Optional[torch.Tensor], what: str, dtype, shape, device) -> Optional[torch.Tensor]:
+    """Check an argument's type, shape, layout and device (None passes)."""
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device):
+        raise QvgError(1, f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t
+
+
+def _batch(p: Packed, Q: torch.Tensor, q_pos: torch.Tensor, k_pos, tail: Optional[Tail], causal: bool, values: bool) -> _Batch:
+    if p.dtype != BF16:
+        raise QvgError(2, "the cache must be a bf16 one")
+    if Q.dim() != 4 or Q.shape[1] % p.H != 0 or Q.shape[3] != p.d:
+        raise QvgError(1, "Q must be a [B][H * group][Nq][d] tensor")
+    dev, (B, Hq, Nq, d) = p.codes.device, Q.shape
+    _device_tensor(Q, "Q", torch.bfloat16, Q.shape, dev)
+    _device_tensor(q_pos, "q_pos", torch.int64, (B, Nq), dev)
+    _device_tensor(k_pos, "k_pos", torch.int64, (p.H, p.N), dev)
+    b = _Batch(B=B, group=Hq // p.H, Nq=Nq, Nt=0, Q=_ptr(Q), q_pos=_ptr(q_pos), k_pos=_ptr(k_pos), causal=1 if causal else 0)
+    if tail is not None and tail.k.dim() == 4 and tail.k.shape[2] > 0:
+        shape = (B, p.H, tail.k.shape[2], d)
+        if values and tail.v is None:
+            raise QvgError(1, "the tail has no values")
+        _device_tensor(tail.k, "the tail's k", torch.bfloat16, shape, dev)
+        _device_tensor(tail.v, "the tail's v", torch.bfloat16, shape, dev)
+        _device_tensor(tail.pos, "the tail's pos", torch.int64, (B, shape[2]), dev)
+        _device_tensor(tail.length, "the tail's length", torch.int32, (B,), dev)
+        b.Nt, b.tail_k, b.tail_v = shape[2], _ptr(tail.k), _ptr(tail.v)
+        b.tail_pos, b.tail_len = _ptr(tail.pos), _ptr(tail.length)
+    elif tail is not None and tail.k.dim() != 4:
+        raise QvgError(1, "the tail's k must be a [B][H][Nt][d] tensor")
+    return b
+
+
+def _on_device(*tensors):
+    """The device of the first tensor, a CUDA one, with the others on it."""
+    dev = tensors[0].device
+    if dev.type != "cuda" or any(t is not None and t.device != dev for t in tensors):
+        raise QvgError(1, "every tensor must be on the cache's CUDA device")
+    return dev
+
+
+def _lent(stream, *tensors):
+    """Tensors allocated here on the current stream whose work runs on `stream`:
+    their memory is not reused before that work is done."""
+    if stream is not None:
+        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        for t in tensors:
+            if t.numel():
+                t.record_stream(s)
+
+
+def _tables(tables: torch.Tensor) -> torch.Tensor:
+    if tables.dtype != torch.uint8 or tables.dim() != 1 or not tables.is_contiguous():
+        raise QvgError(1, "tables must be a tensor of rope_tables")
+    return tables
+
+
+def _batch_workspace(workspace, need: int, device, stream):
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        _lent(stream, workspace)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
+        raise QvgError(1, f"the workspace must be a contiguous uint8 tensor on {device}")
+    return workspace
+
+
+def attention_batch(kp: Packed, vp: Packed, Q: torch.Tensor, q_pos: torch.Tensor, tables: torch.Tensor,
+                    tail: Optional[Tail] = None, k_pos: Optional[torch.Tensor] = None, causal: bool = False,
+                    O: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """qvg_attention_batch: attention of B sequences over the compressed prefix
+    they share (kp, vp: H blocks), joined with each one's own tail.
+    Q [B][H * group][Nq][d] bf16 and q_pos [B][Nq] int64 (negative: a padding
+    row); k_pos [H][N] int64, the cached tokens' positions (None: 0 .. N-1);
+    returns O, like Q, zeros in rows that see no key.  `workspace`: a uint8
+    tensor of attention_batch_workspace_bytes (None: allocated here)."""
+    b = _batch(kp, Q, q_pos, k_pos, tail, causal, True)
+    if (vp.N, vp.H, vp.d, vp.dtype) != (kp.N, kp.H, kp.d, kp.dtype) or bytes(vp.cfg) != bytes(kp.cfg):
+        raise QvgError(1, "kp and vp must have the same sizes and configuration")
+    _device_tensor(O, "O", torch.bfloat16, Q.shape, Q.device)
+    dev = _on_device(kp.codes, vp.codes, _tables(tables))
+    with torch.cuda.device(dev):
+        need = 0 if workspace is not None else int(
+            lib().qvg_attention_batch_workspace_bytes(C.byref(kp.cfg), kp.N, kp.H, C.byref(b)))
+        ws = _batch_workspace(workspace, need, dev, stream)
+        if O is None:
+            O = torch.empty_like(Q)
+            _lent(stream, O)
+        ks, vs = kp.struct(), vp.struct()
+        _check(lib().qvg_attention_batch(C.byref(kp.cfg), C.byref(ks), C.byref(vs), kp.N, kp.H, kp.d, C.byref(b),
+                                         _ptr(tables), tables.numel(), _ptr(O), _ptr(ws), ws.numel(), _stream(stream)),
+               "qvg_attention_batch")
+    return O
+
+
+def attention_weights(kp: Packed, Q: torch.Tensor, q_pos: torch.Tensor, tables: torch.Tensor,
+                      received: Optional[torch.Tensor] = None, tail: Optional[Tail] = None,
+                      k_pos: Optional[torch.Tensor] = None, causal: bool = False, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """qvg_attention_weights: received [H][N] fp32 (None: zeros) plus the softmax
+    weight that each token of the prefix gets from the batch's rows (arguments
+    as attention_batch).  `out` may be `received`, to add in place."""
+    b = _batch(kp, Q, q_pos, k_pos, tail, causal, False)
+    _device_tensor(out, "out", torch.float32, (kp.H, kp.N), Q.device)
+    _device_tensor(received, "received", torch.float32, (kp.H, kp.N), Q.device)
+    dev = _on_device(kp.codes, _tables(tables))
+    with torch.cuda.device(dev):
+        need = 0 if workspace is not None else int(
+            lib().qvg_attention_weights_workspace_bytes(C.byref(kp.cfg), kp.N, kp.H, C.byref(b)))
+        ws = _batch_workspace(workspace, need, dev, stream)
+        if out is None:
+            out = torch.empty((kp.H, kp.N), dtype=torch.float32, device=dev)
+            _lent(stream, out)
+        ks = kp.struct()
+        _check(lib().qvg_attention_weights(C.byref(kp.cfg), C.byref(ks), kp.N, kp.H, kp.d, C.byref(b), _ptr(tables),
+                                           tables.numel(), _ptr(received), _ptr(out), _ptr(ws), ws.numel(),
+                                           _stream(stream)),
+               "qvg_attention_weights")
+    return out
+
+
+def _batch_sizes(B: int, group: int, Nq: int, Nt: int) -> _Batch:
+    return _Batch(B=B, group=group, Nq=Nq, Nt=Nt)
+
+
+def attention_batch_workspace_bytes(cfg: Config, Nk: int, H: int, B: int, group: int, Nq: int, Nt: int = 0) -> int:
+    """qvg_attention_batch_workspace_bytes for these sizes."""
+    return int(lib().qvg_attention_batch_workspace_bytes(C.byref(cfg), Nk, H, C.byref(_batch_sizes(B, group, Nq, Nt))))
+
+
+def attention_weights_workspace_bytes(cfg: Config, Nk: int, H: int, B: int, group: int, Nq: int, Nt: int = 0) -> int:
+    """qvg_attention_weights_workspace_bytes for these sizes."""
+    return int(lib().qvg_attention_weights_workspace_bytes(C.byref(cfg), Nk, H, C.byref(_batch_sizes(B, group, Nq, Nt))))
+
+
+@dataclass
+class Evicted:
+    """What evict leaves: the closed-up caches, and of every kept token its
+    index before, its position and its weight."""
+    k: Packed
+    v: Packed
+    kept: torch.Tensor        # [H][keep] int32, ascending
+    pos: torch.Tensor         # [H][keep] int64
+    weights: torch.Tensor     # [H][keep] fp32
+
+
+def _closed(p: Packed, keep: int) -> Packed:
+    """Streams for `keep` tokens a head beside p's own centroid tables."""
+    ng, T = p.d // p.cfg.group_size, p.cfg.T
+    u8 = dict(dtype=torch.uint8, device=p.codes.device)
+    return Packed(codes=torch.empty((p.H, keep, p.d // 4), **u8), scale=torch.empty((p.H, keep, ng), **u8),
+                  zero=torch.empty((p.H, keep, ng) if p.cfg.scale_mode == ASYM else (0,), **u8),
+                  assign=torch.empty((T, p.H, keep), **u8), centroids=p.centroids,
+                  cfg=p.cfg, N=keep, H=p.H, d=p.d, dtype=p.dtype)
+
+
+def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int = 0, recent: int = 0,
+          k_pos: Optional[torch.Tensor] = None, stream=None) -> Evicted:
+    """qvg_evict: keep the first `first` and the last `recent` tokens of every
+    head and, up to `keep` in all, those with the largest weights [H][N] fp32.
+    The caches returned share the centroid tables of kp and vp."""
+    if (vp.N, vp.H, vp.d) != (kp.N, kp.H, kp.d) or bytes(vp.cfg) != bytes(kp.cfg):
+        raise QvgError(1, "kp and vp must have the same sizes and configuration")
+    if not 1 <= keep <= kp.N or first < 0 or recent < 0 or first + recent > keep:
+        raise QvgError(1, "keep must be 1 .. N, first + recent at most keep")
+    _device_tensor(weights, "weights", torch.float32, (kp.H, kp.N), kp.codes.device)
+    _device_tensor(k_pos, "k_pos", torch.int64, (kp.H, kp.N), kp.codes.device)
+    dev = _on_device(kp.codes, vp.codes)
+    with torch.cuda.device(dev):
+        e = Evicted(k=_closed(kp, keep), v=_closed(vp, keep),
+                    kept=torch.empty((kp.H, keep), dtype=torch.int32, device=dev),
+                    pos=torch.empty((kp.H, keep), dtype=torch.int64, device=dev),
+                    weights=torch.empty((kp.H, keep), dtype=torch.float32, device=dev))
+        _lent(stream, e.kept, e.pos, e.weights,
+              *(t for p in (e.k, e.v) for t in (p.codes, p.scale, p.zero, p.assign)))
+        ks, vs, ko, vo = kp.struct(), vp.struct(), e.k.struct(), e.v.struct()
+        _check(lib().qvg_evict(C.byref(kp.cfg), C.byref(ks), C.byref(vs), kp.N, kp.H, kp.d, _ptr(weights), _ptr(k_pos), keep,
+                               first, recent, C.byref(ko), C.byref(vo), _ptr(e.kept), _ptr(e.pos), _ptr(e.weights),
+                               _stream(stream)),
+               "qvg_evict")
+    return e
 
 
 def profile_enable(on: bool = True):

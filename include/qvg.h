@@ -41,8 +41,9 @@
  *                qvg_cache_create_adaptive fails (QVG_ERR_NO_MEMORY, nothing
  *                allocated);
  *       stream   the quantising calls (qvg_quantize, qvg_quantize_static,
- *                both appends), qvg_dequantize, qvg_cache_dequantize and
- *                qvg_attention report QVG_ERR_CUDA after queueing, as a
+ *                both appends), qvg_dequantize, qvg_cache_dequantize,
+ *                qvg_attention, qvg_attention_batch, qvg_attention_weights
+ *                and qvg_evict report QVG_ERR_CUDA after queueing, as a
  *                failed launch would (an append then leaves the cache
  *                unchanged);
  *       timeout  the first CTA of the tensor-core assignment withholds one
@@ -329,6 +330,111 @@ QVG_API qvg_status qvg_attention(const qvg_config* cfg, const qvg_packed* k, con
 QVG_API int32_t qvg_attention_set_split(int32_t split);
 QVG_API int32_t qvg_attention_split(const qvg_config* cfg, int64_t Nk, int32_t H, int64_t Nq, size_t ws_bytes);
 QVG_API size_t qvg_attention_workspace_bytes(const qvg_config* cfg, int64_t Nk, int32_t H, int64_t Nq);
+
+/* ------------------------------------------------------------------ */
+/* A batch that shares a compressed prefix, and a cache within a budget  */
+/* (no counterpart in the method: what serving from such a cache needs). */
+/* ------------------------------------------------------------------ */
+
+/* The queries of B sequences that share one compressed prefix of H blocks
+ * (K/V heads) of Nk tokens, and what each sequence has of its own.
+ * All DEVICE pointers, 16-byte aligned, contiguous.
+ *   Q         [B][H * group][Nq][d] bf16, before the rotary embedding; query
+ *             heads h * group .. h * group + group - 1 read K/V head h
+ *   q_pos     [B][Nq] positions; a negative one marks a padding row, which
+ *             sees no key
+ *   k_pos     [H][Nk] positions of the cached tokens (as qvg_evict leaves
+ *             them), in any order; NULL: token i at position i
+ *   Nt        tokens of room in each sequence's tail, its own newest tokens,
+ *             not compressed; 0: no tails (the tail pointers are not read)
+ *   tail_k    [B][H][Nt][d] bf16, before the rotary embedding
+ *   tail_v    [B][H][Nt][d] bf16 (not read by qvg_attention_weights)
+ *   tail_pos  [B][Nt]; NULL: tail token i at position Nk + i
+ *   tail_len  [B] tokens each tail holds (clamped to 0 .. Nt); NULL: Nt.  What
+ *             lies behind them is not used and may hold anything
+ *   causal    1: a query sees the keys at positions not above its own;
+ *             0: every key of the prefix and of its tail
+ * Positions outside [0, max_pos] of the rotary tables are clamped for the
+ * rotation; masks compare the positions themselves, clamped to 32 bits.
+ * Keys and values that a row is masked from still have to be finite, except
+ * those behind a tail's length. */
+typedef struct {
+    int32_t B, group;
+    int64_t Nq, Nt;
+    const void* Q;
+    const int64_t* q_pos;
+    const int64_t* k_pos;
+    const void* tail_k;
+    const void* tail_v;
+    const int64_t* tail_pos;
+    const int32_t* tail_len;
+    int32_t causal;
+} qvg_batch;
+
+/* Softmax attention of a batch over its shared prefix and the sequences' own
+ * tails, the prefix reconstructed once for the rows of all sequences and of
+ * all query heads of a K/V head:
+ *   O[b][j][n] = softmax(rope(Q[b][j][n]) rope([K^[h]; tail_k[b][h]])^T / sqrt(d)) [V^[h]; tail_v[b][h]]
+ * with h = j / group.  K^ and V^ are what qvg_dequantize would write for `k`
+ * and `v` (two packed forms of H blocks of Nk tokens with the same cfg; bf16).
+ * A row that sees no key gets zeros.
+ *   O  DEVICE [B][H * group][Nq][d] bf16, 16-byte aligned
+ *   workspace, ws_bytes  DEVICE scratch for the partial results of the ranges
+ *      that the keys are cut into, 16-byte aligned, not shared with calls
+ *      that may run at the same time (two captured graphs among them)
+ * The products have bf16 operands (rotated queries and keys and the softmax
+ * weights are rounded to bf16) and fp32 sums.
+ * Errors: INVALID_ARG (also Nk < 1, Nq < 1, B < 1, group < 1, Nt < 0, or
+ * tables that do not cover Nk - 1 when k_pos is NULL), UNSUPPORTED (d != 128,
+ * B * group * Nq or Nt of 2^23 or more), WORKSPACE_TOO_SMALL, CUDA,
+ * DEVICE_TIMEOUT (recorded in the tables' status word by earlier work). */
+QVG_API qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* k, const qvg_packed* v, int64_t Nk,
+                               int32_t H, int32_t d, const qvg_batch* batch, const void* tables,
+                               size_t tables_bytes, void* O, void* workspace, size_t ws_bytes,
+                               qvg_stream_t stream);
+
+/* The attention weight that every token of the shared prefix receives from a
+ * batch, added to what it received before:
+ *   out[h][j] = received[h][j] + sum over the rows of head h of softmax(...)_j
+ * with the softmax of qvg_attention_batch (over the prefix and the row's own
+ * tail).  Each product is taken from operands of 16 mantissa bits (the high
+ * and low bf16 halves of rotated queries and keys) and every sum in fp32, in
+ * an order that does not depend on the launch, so equal calls give equal bits.
+ *   received  DEVICE [H][Nk] fp32, or NULL: zeros
+ *   out       DEVICE [H][Nk] fp32; may be `received` itself
+ * Only `k` of the cache is read.  Workspace and errors as qvg_attention_batch. */
+QVG_API qvg_status qvg_attention_weights(const qvg_config* cfg, const qvg_packed* k, int64_t Nk, int32_t H, int32_t d,
+                                 const qvg_batch* batch, const void* tables, size_t tables_bytes,
+                                 const float* received, float* out, void* workspace, size_t ws_bytes,
+                                 qvg_stream_t stream);
+
+/* The workspace the two calls above need on the current device (its pointers
+ * in `batch` are not read); 0 for invalid arguments or without a device. */
+QVG_API size_t qvg_attention_batch_workspace_bytes(const qvg_config* cfg, int64_t Nk, int32_t H,
+                                           const qvg_batch* batch);
+QVG_API size_t qvg_attention_weights_workspace_bytes(const qvg_config* cfg, int64_t Nk, int32_t H,
+                                             const qvg_batch* batch);
+
+/* Keep `keep` tokens of every head of a compressed cache and close its packed
+ * streams up over the others: the first `first` and the last `recent` tokens
+ * stay, then those with the largest weights (of equal weights the token with
+ * the lower index; NaN ranks below everything).  The kept tokens stay in
+ * order.  Nothing is quantised again: the centroid tables stay as they are (the
+ * `centroids` of the outputs are not accessed: let them be those of the
+ * inputs), and a kept token's reconstruction is the same bit for bit.
+ *   weights  DEVICE [H][Nk] fp32 (as qvg_attention_weights accumulates them)
+ *   k_pos    DEVICE [H][Nk], or NULL: token i at position i
+ *   k_out, v_out  packed forms of H blocks of `keep` tokens (DEVICE, codes
+ *            16-byte aligned, no overlap with the inputs)
+ *   kept     DEVICE [H][keep]: the kept tokens' indices, ascending
+ *   pos_out  DEVICE [H][keep]: their positions, or NULL
+ *   weights_out  DEVICE [H][keep]: their weights, or NULL
+ * Errors: INVALID_ARG (also keep < 1, keep > Nk, first + recent > keep, or an
+ * output that is its input), UNSUPPORTED, CUDA. */
+QVG_API qvg_status qvg_evict(const qvg_config* cfg, const qvg_packed* k, const qvg_packed* v, int64_t Nk, int32_t H,
+                     int32_t d, const float* weights, const int64_t* k_pos, int64_t keep, int64_t first,
+                     int64_t recent, const qvg_packed* k_out, const qvg_packed* v_out, int32_t* kept,
+                     int64_t* pos_out, float* weights_out, qvg_stream_t stream);
 
 /* ------------------------------------------------------------------ */
 /* Diagnostics (no counterpart in the method; used by the benchmark).    */

@@ -15,12 +15,6 @@
 #include "qvg_launch.h"
 
 namespace qvg {
-namespace {
-
-constexpr int kPosNever = 0x7FFFFFFF;             // a key that no row sees (past the end)
-constexpr int kLimitAll = 0x7FFFFFFE;             // a row that sees every key
-constexpr int kLimitNone = -0x7FFFFFFF - 1;       // a row that sees none
-constexpr float kNoMax = -3.0e38f;                // row maximum before any key
 
 struct BatchParams {
   const uint8_t* codes[2];        // K, V: [H][Nk][d/4]
@@ -45,6 +39,18 @@ struct BatchParams {
   float* part_O;                  // [S1 + S2][H][R][d]: unnormalised O of each range
   float2* part_ml;                // [S1 + S2][H][R]: (row maximum, row sum) of each range, base 2
 };
+
+// The tensor-core kernels' plans (into tiles1, tiles2, S1 and S2) and launches.
+int plan_batch_tc(BatchParams& p);                 // returns the CTAs per cluster
+cudaError_t launch_batch_tc(const BatchParams& p, int pair, void* tables, cudaStream_t s);
+
+namespace {
+
+constexpr int kPosNever = 0x7FFFFFFF;             // a key that no row sees (past the end)
+constexpr int kLimitAll = 0x7FFFFFFE;             // a row that sees every key
+constexpr int kLimitNone = -0x7FFFFFFF - 1;       // a row that sees none
+constexpr float kNoMax = -3.0e38f;                // row maximum before any key
+
 
 __device__ __forceinline__ int clamp_pos(int64_t pos) {
   return (int)(pos < -0x7FFFFFFFll ? -0x7FFFFFFFll : pos > 0x7FFFFFFDll ? 0x7FFFFFFDll : pos);

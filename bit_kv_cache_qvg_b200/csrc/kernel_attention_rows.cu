@@ -523,6 +523,10 @@ void plan_rows(BatchParams& p) {
   p.S2 = p.Nt > 0 ? (int)std::max<int64_t>(1, std::min<int64_t>({most2, (p.S1 * p.Nt + p.Nk - 1) / p.Nk, 64})) : 0;
 }
 
+// Rows beyond which the tcgen05 kernels take over.
+constexpr int64_t kManyRows = 48;
+bool many_rows(const BatchParams& p) { return p.R > kManyRows; }
+
 BatchParams params_of(const BatchArgs& a) {
   BatchParams p{};
   for (int w = 0; w < 2; ++w) {
@@ -580,7 +584,8 @@ cudaError_t launch_rows(const BatchParams& p, cudaStream_t s) {
 
 size_t attention_batch_workspace_bytes(const BatchArgs& a) {
   BatchParams p = params_of(a);
-  plan_rows(p);
+  if (many_rows(p)) plan_batch_tc(p);
+  else plan_rows(p);
   return partial_bytes(p, true);
 }
 
@@ -592,9 +597,16 @@ size_t attention_weights_workspace_bytes(const BatchArgs& a) {
 
 cudaError_t launch_attention_batch(const BatchArgs& a, void* O, void* ws, cudaStream_t s) {
   BatchParams p = params_of(a);
-  plan_rows(p);
-  place_partials(p, ws, true);
-  const cudaError_t e = launch_rows<true>(p, s);
+  cudaError_t e;
+  if (many_rows(p)) {
+    const int pair = plan_batch_tc(p);
+    place_partials(p, ws, true);
+    e = launch_batch_tc(p, pair, const_cast<void*>(a.tables), s);
+  } else {
+    plan_rows(p);
+    place_partials(p, ws, true);
+    e = launch_rows<true>(p, s);
+  }
   if (e != cudaSuccess) return e;
   qvg_batch_merge<<<(unsigned)((p.R * p.H + 3) / 4), 128, 0, s>>>(p, static_cast<__nv_bfloat16*>(O));
   return cudaGetLastError();

@@ -34,15 +34,33 @@ struct BatchParams {
   int64_t R, RB;                  // rows per K/V head, and of one sequence
   int B, H, K, T, G, lgG, sym, causal;
   float sl;                       // log2(e) / sqrt(d)
-  int S1, S2;                     // ranges of the prefix and of each tail
-  int64_t tiles1, tiles2;         // row tiles of a head, and of one sequence's rows
-  float* part_O;                  // [S1 + S2][H][R][d]: unnormalised O of each range
-  float2* part_ml;                // [S1 + S2][H][R]: (row maximum, row sum) of each range, base 2
+  // The keys are cut into ranges, each with a slot of partial results: the
+  // prefix's from slot 0, the tails' from slot2.  A launch handles S1 ranges of
+  // the prefix and S2 of every tail (0: another launch does).
+  int S1, S2, slot2, slots;
+  int64_t tiles1, tiles2;         // this launch's row tiles of a head, and of one sequence's rows
+  float* part_O;                  // [slots][H][R][d]: unnormalised O of each range
+  float2* part_ml;                // [slots][H][R]: (row maximum, row sum) of each range, base 2
+  __nv_bfloat16* O;               // where a single slot needs no merge
+  // Tensor-core operands of heads h0 .. h0 + Hn - 1, laid out as the kernels'
+  // shared memory wants them (kernel_batch_expand.cu).
+  int h0, Hn;
+  int64_t nt1, nt2;               // tiles of 128 keys of the prefix and of a tail
+  int64_t Rp, RBp;                // rows of a head, and of one sequence, padded to 256
+  uint8_t* key_img[2];            // prefix, tails: [Hn][nt1], [B][Hn][nt2] tiles of 32 KB
+  uint8_t* val_img[2];            // the same of V (or of the keys' low halves)
+  uint8_t* row_img[2];            // rows by head [Hn][2][Rp][128 B], and by sequence [B][Hn][2][RBp][128 B]
+  uint8_t* row_lo[2];             // the rows' low halves
+  uint32_t* status;
 };
 
-// The tensor-core kernels' plans (into tiles1, tiles2, S1 and S2) and launches.
-int plan_batch_tc(BatchParams& p);                 // returns the CTAs per cluster
-cudaError_t launch_batch_tc(const BatchParams& p, int pair, void* tables, cudaStream_t s);
+constexpr int64_t kImageBytes = 128 * kD * 2;     // one 128 x 128 bf16 operand tile
+
+cudaError_t launch_rows_partial(const BatchParams& p, bool values, cudaStream_t s);      // kernel_attention_rows.cu
+cudaError_t launch_rows_weights(const BatchParams& p, const float* received, float* out, cudaStream_t s);
+cudaError_t launch_batch_merge(const BatchParams& p, cudaStream_t s);
+cudaError_t launch_batch_expand(const BatchParams& p, bool precise, cudaStream_t s);     // kernel_batch_expand.cu
+cudaError_t launch_batch_attend(const BatchParams& p, cudaStream_t s);                   // kernel_batch_attend.cu
 
 namespace {
 
@@ -72,6 +90,16 @@ __device__ __forceinline__ int row_limit(const BatchParams& p, int64_t pos) {
 __device__ __forceinline__ int64_t tail_length(const BatchParams& p, int b) {
   const int64_t n = p.tail_len != nullptr ? (int64_t)__ldg(p.tail_len + b) : p.Nt;
   return n < 0 ? 0 : n < p.Nt ? n : p.Nt;
+}
+
+// Row of the rotary table and position for the masks of key `key` (below the
+// count n) of head h's prefix, or of sequence b's tail.
+__device__ __forceinline__ int64_t raw_key_pos(const BatchParams& p, bool tail, int h, int b, int64_t key) {
+  if (tail) return p.tail_pos != nullptr ? __ldg(p.tail_pos + (int64_t)b * p.Nt + key) : p.Nk + key;
+  return p.k_pos != nullptr ? __ldg(p.k_pos + (int64_t)h * p.Nk + key) : key;
+}
+__device__ __forceinline__ int mask_pos(const BatchParams& p, bool tail, int h, int b, int64_t key, int64_t n) {
+  return key < n ? clamp_pos(raw_key_pos(p, tail, h, b, key)) : kPosNever;
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -15,8 +15,6 @@
 // read 64 contiguous bytes of a centroid row.  In the product with V the lane
 // owns chunks g and g + 8 of its keys.  With few rows nothing is shared
 // between warps, so nothing goes through shared memory but the queries.
-#include <algorithm>
-
 #include "batch.cuh"
 
 namespace qvg {
@@ -107,7 +105,7 @@ __device__ __forceinline__ void rotated_key(const BatchParams& p, const float2* 
                                             F&& use) {
   const bool in = key < ks.n;
   const int64_t tok = in ? key : ks.n - 1;
-  int64_t pos;
+  const int64_t pos = raw_key_pos(p, ks.tail, ks.h, ks.b, tok);
   uint16_t code[4];
   uint4 sc = make_uint4(0, 0, 0, 0), ze = make_uint4(0, 0, 0, 0);
   int kk[TT > 0 ? TT : 1];
@@ -115,10 +113,8 @@ __device__ __forceinline__ void rotated_key(const BatchParams& p, const float2* 
   const int64_t row = (int64_t)ks.h * p.Nk + tok;
   const __nv_bfloat16* dense = nullptr;
   if (ks.tail) {
-    pos = p.tail_pos != nullptr ? __ldg(p.tail_pos + (int64_t)ks.b * p.Nt + tok) : p.Nk + tok;
     dense = p.tail[0] + (((int64_t)ks.b * p.H + ks.h) * p.Nt + tok) * kD;
   } else {
-    pos = p.k_pos != nullptr ? __ldg(p.k_pos + row) : tok;
 #pragma unroll
     for (int i = 0; i < 4; ++i) code[i] = __ldg(reinterpret_cast<const uint16_t*>(p.codes[0] + row * (kD / 4)) + 4 * i + c);
     sc = load_groups(p.scale[0], row, ng);
@@ -149,13 +145,6 @@ __device__ __forceinline__ void rotated_key(const BatchParams& p, const float2* 
     }
     use(i, hi, lo);
   }
-}
-
-// Position of a key for the masks (kPosNever past the end).
-__device__ __forceinline__ int key_pos(const BatchParams& p, const Keys& ks, int64_t key) {
-  if (key >= ks.n) return kPosNever;
-  if (ks.tail) return clamp_pos(p.tail_pos != nullptr ? __ldg(p.tail_pos + (int64_t)ks.b * p.Nt + key) : p.Nk + key);
-  return clamp_pos(p.k_pos != nullptr ? __ldg(p.k_pos + (int64_t)ks.h * p.Nk + key) : key);
 }
 
 // Chunk g + 8 i of a value, as packed bf16 pairs (zero past the end: the
@@ -239,7 +228,7 @@ __device__ __forceinline__ Place place_of(const BatchParams& p, int64_t id) {
   a.ks.h = (int)(unit % p.H);
   a.ks.b = (int)(unit / p.H);
   a.ks.n = a.ks.tail ? tail_length(p, a.ks.b) : p.Nk;
-  a.slot = a.ks.tail ? p.S1 + range : range;
+  a.slot = a.ks.tail ? p.slot2 + range : range;
   a.r0 = (a.ks.tail ? a.ks.b * p.RB : 0) + tile * kRwRows;
   a.r1 = a.ks.tail ? (a.ks.b + 1) * p.RB : p.R;
   const int64_t steps = (a.ks.n + kRwStep - 1) / kRwStep;
@@ -304,7 +293,7 @@ __global__ void __launch_bounds__(kRwThreads) qvg_attention_rows(const BatchPara
       });
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool sees = key_pos(p, a.ks, k + 8 * nt + 2 * c + (e & 1)) <= limit[e >> 1];
+        const bool sees = mask_pos(p, a.ks.tail, a.ks.h, a.ks.b, k + 8 * nt + 2 * c + (e & 1), a.ks.n) <= limit[e >> 1];
         s[nt][e] = sees ? s[nt][e] * p.sl : -INFINITY;
         mt[e >> 1] = fmaxf(mt[e >> 1], s[nt][e]);
       }
@@ -404,7 +393,7 @@ __global__ void __launch_bounds__(kRwThreads) qvg_attention_rows(const BatchPara
 // log2 of a row's sum of 2^(sl s) over every range, from the partial results
 // (a row that sees nothing: +inf, so that every weight 2^(x - inf) is 0).
 __device__ __forceinline__ float row_lse(const BatchParams& p, int h, int64_t r) {
-  const int S = p.S1 + p.S2;
+  const int S = p.slots;
   float M = kNoMax, L = 0.0f;
   for (int s = 0; s < S; ++s) M = fmaxf(M, __ldg(p.part_ml + ((int64_t)s * p.H + h) * p.R + r).x);
   for (int s = 0; s < S; ++s) {
@@ -449,7 +438,7 @@ __global__ void __launch_bounds__(kRwThreads) qvg_weights_rows(const BatchParams
         for (int e = 0; e < 4; ++e) { kh[4 * i + e] = hi[e]; kl[4 * i + e] = lo[e]; }
       });
       const int64_t j = k + 8 * nt + 2 * c;
-      const int pos[2] = {key_pos(p, ks, j), key_pos(p, ks, j + 1)};
+      const int pos[2] = {mask_pos(p, false, ks.h, 0, j, p.Nk), mask_pos(p, false, ks.h, 0, j + 1, p.Nk)};
       float sum[2] = {0.0f, 0.0f};
 #pragma unroll 1
       for (int t = 0; t < tiles; ++t) {
@@ -487,13 +476,13 @@ __global__ void __launch_bounds__(kRwThreads) qvg_weights_rows(const BatchParams
 // The ranges of every row joined: O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
 // with M = max_s m_s, rounded to bf16; zeros for a row that sees nothing.  A
 // warp per row, a lane per four channels.
-__global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p, __nv_bfloat16* O) {
+__global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p) {
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   if (row >= p.R * p.H) return;
   const int h = (int)(row / p.R);
   const int64_t r = row - (int64_t)h * p.R;
-  const int S = p.S1 + p.S2;
+  const int S = p.slots;
   float M = kNoMax;
   for (int s = 0; s < S; ++s) M = fmaxf(M, __ldg(p.part_ml + s * p.R * p.H + row).x);
   float L = 0.0f;
@@ -507,68 +496,13 @@ __global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p, __nv
     L += w * ml.y;
   }
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  reinterpret_cast<uint2*>(O + query_row(p, h, r) * kD)[lane] =
+  reinterpret_cast<uint2*>(p.O + query_row(p, h, r) * kD)[lane] =
       make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
-}
-
-// Ranges of keys: enough CTAs to fill the SMs four times over, at least
-// kRwStep keys to each.
-void plan_rows(BatchParams& p) {
-  const int64_t target = 4 * (int64_t)device_sm_count();
-  p.tiles1 = (p.R + kRwRows - 1) / kRwRows;
-  p.tiles2 = (p.RB + kRwRows - 1) / kRwRows;
-  const int64_t most1 = (p.Nk + kRwStep - 1) / kRwStep, most2 = (p.Nt + kRwStep - 1) / kRwStep;
-  const int64_t s1 = (target + p.tiles1 * p.H - 1) / (p.tiles1 * p.H);
-  p.S1 = (int)std::max<int64_t>(1, std::min<int64_t>({s1, most1, 64}));
-  p.S2 = p.Nt > 0 ? (int)std::max<int64_t>(1, std::min<int64_t>({most2, (p.S1 * p.Nt + p.Nk - 1) / p.Nk, 64})) : 0;
-}
-
-// Rows beyond which the tcgen05 kernels take over.
-constexpr int64_t kManyRows = 48;
-bool many_rows(const BatchParams& p) { return p.R > kManyRows; }
-
-BatchParams params_of(const BatchArgs& a) {
-  BatchParams p{};
-  for (int w = 0; w < 2; ++w) {
-    const qvg_packed* pk = w == 0 ? a.k : a.v;
-    if (pk == nullptr) continue;
-    p.codes[w] = pk->codes; p.scale[w] = pk->scale; p.zero[w] = pk->zero; p.assign[w] = pk->assign;
-    p.tab[w] = static_cast<const __nv_bfloat16*>(pk->centroids);
-  }
-  const qvg_batch& q = *a.batch;
-  p.Q = static_cast<const __nv_bfloat16*>(q.Q);
-  p.q_pos = q.q_pos;
-  p.k_pos = q.k_pos;
-  p.tail[0] = static_cast<const __nv_bfloat16*>(q.tail_k);
-  p.tail[1] = static_cast<const __nv_bfloat16*>(q.tail_v);
-  p.tail_pos = q.tail_pos;
-  p.tail_len = q.tail_len;
-  p.rope = reinterpret_cast<const float2*>(static_cast<const char*>(a.tables) + kRopeHeaderBytes);
-  p.max_pos = a.max_pos;
-  p.Nk = a.Nk; p.Nq = q.Nq; p.Nt = q.Nt;
-  p.RB = q.group * q.Nq;
-  p.R = q.B * p.RB;
-  p.B = q.B; p.H = a.H; p.K = a.K; p.T = a.T; p.G = a.G; p.sym = a.sym; p.causal = q.causal;
-  for (int g = a.G; g > 1; g >>= 1) ++p.lgG;
-  p.sl = 1.4426950408889634f / sqrtf((float)kD);
-  return p;
-}
-
-// The partial results in the workspace: O (attention only), then (maximum, sum).
-size_t partial_bytes(const BatchParams& p, bool values) {
-  return (size_t)(p.S1 + p.S2) * p.H * p.R * ((values ? kD * sizeof(float) : 0) + sizeof(float2));
-}
-void place_partials(BatchParams& p, void* ws, bool values) {
-  p.part_O = static_cast<float*>(ws);
-  p.part_ml = reinterpret_cast<float2*>(p.part_O + (values ? (size_t)(p.S1 + p.S2) * p.H * p.R * kD : 0));
-}
-int64_t rows_grid(const BatchParams& p) {
-  return p.S1 * p.tiles1 * p.H + p.S2 * p.tiles2 * p.H * p.B;
 }
 
 template <bool VALUES>
 cudaError_t launch_rows(const BatchParams& p, cudaStream_t s) {
-  const unsigned grid = (unsigned)rows_grid(p);
+  const unsigned grid = (unsigned)(p.S1 * p.tiles1 * p.H + p.S2 * p.tiles2 * p.H * p.B);
   switch (p.T) {
     case 0: qvg_attention_rows<0, VALUES><<<grid, kRwThreads, 0, s>>>(p); break;
     case 1: qvg_attention_rows<1, VALUES><<<grid, kRwThreads, 0, s>>>(p); break;
@@ -582,42 +516,11 @@ cudaError_t launch_rows(const BatchParams& p, cudaStream_t s) {
 
 }  // namespace
 
-size_t attention_batch_workspace_bytes(const BatchArgs& a) {
-  BatchParams p = params_of(a);
-  if (many_rows(p)) plan_batch_tc(p);
-  else plan_rows(p);
-  return partial_bytes(p, true);
+cudaError_t launch_rows_partial(const BatchParams& p, bool values, cudaStream_t s) {
+  return values ? launch_rows<true>(p, s) : launch_rows<false>(p, s);
 }
 
-size_t attention_weights_workspace_bytes(const BatchArgs& a) {
-  BatchParams p = params_of(a);
-  plan_rows(p);
-  return partial_bytes(p, false);
-}
-
-cudaError_t launch_attention_batch(const BatchArgs& a, void* O, void* ws, cudaStream_t s) {
-  BatchParams p = params_of(a);
-  cudaError_t e;
-  if (many_rows(p)) {
-    const int pair = plan_batch_tc(p);
-    place_partials(p, ws, true);
-    e = launch_batch_tc(p, pair, const_cast<void*>(a.tables), s);
-  } else {
-    plan_rows(p);
-    place_partials(p, ws, true);
-    e = launch_rows<true>(p, s);
-  }
-  if (e != cudaSuccess) return e;
-  qvg_batch_merge<<<(unsigned)((p.R * p.H + 3) / 4), 128, 0, s>>>(p, static_cast<__nv_bfloat16*>(O));
-  return cudaGetLastError();
-}
-
-cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, float* out, void* ws, cudaStream_t s) {
-  BatchParams p = params_of(a);
-  plan_rows(p);
-  place_partials(p, ws, false);
-  const cudaError_t e = launch_rows<false>(p, s);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_rows_weights(const BatchParams& p, const float* received, float* out, cudaStream_t s) {
   const unsigned grid = (unsigned)((p.Nk + kRwStep - 1) / kRwStep * p.H);
   switch (p.T) {
     case 0: qvg_weights_rows<0><<<grid, kRwThreads, 0, s>>>(p, received, out); break;
@@ -627,6 +530,11 @@ cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, 
     case 4: qvg_weights_rows<4><<<grid, kRwThreads, 0, s>>>(p, received, out); break;
     default: qvg_weights_rows<-1><<<grid, kRwThreads, 0, s>>>(p, received, out);
   }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_batch_merge(const BatchParams& p, cudaStream_t s) {
+  qvg_batch_merge<<<(unsigned)((p.R * p.H + 3) / 4), 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 

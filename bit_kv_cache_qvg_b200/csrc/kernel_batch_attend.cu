@@ -1,0 +1,544 @@
+// kernel_batch_attend.cu -- qvg_attention_batch for many rows: softmax
+// attention over the operand tiles that kernel_batch_expand.cu wrote, on
+// tcgen05; and the plans and launches of qvg_attention_batch and
+// qvg_attention_weights.
+//
+// One CTA = 256 rows of one K/V head (two row tiles of 128) x a range of key
+// tiles, of the prefix (the rows of every sequence and query head share it)
+// or of one sequence's tail.  Ten warps:
+//   * one thread streams K and V tiles (32 KB bulk copies) through a ring of
+//     five slots, K0 V0 K1 V1 ...;
+//   * one thread issues the products, S_g = Q_g K'^T and O_g += P_g V for the
+//     two row tiles g = 0, 1 in turn (kind::f16, M = N = K = 128, fp32
+//     accumulators in tensor memory; P read from tensor memory).  P_g lies over
+//     S_g's columns: the products run in the order they are issued, so S_g of
+//     the next tile follows O_g of this one without a wait;
+//   * four warps per row tile run its softmax, a thread per row, the row's 128
+//     scores in registers: while one tile's softmax runs, the other's products
+//     do.  The reference maximum rises only when a row's maximum exceeds it by
+//     more than 8 (base 2), so O is rescaled rarely.
+// Every wait is bounded and gives up when another role has; the kernel then
+// records QVG_ERR_DEVICE_TIMEOUT in the tables' status word.
+#include <algorithm>
+#include <type_traits>
+
+#include "attention_tc.cuh"
+#include "batch.cuh"
+
+namespace qvg {
+namespace {
+
+constexpr int kAdThreads = 320;                   // 8 softmax warps, the issuer's, the loader's
+constexpr int kAdRows = 256;                      // rows per CTA
+constexpr int kAdSlots = 5;                       // ring of operand tiles
+constexpr int kAdMaxRanges = 16;                  // of the prefix
+
+struct __align__(8) AdShared {
+  uint64_t full[kAdSlots], empty[kAdSlots];
+  uint64_t q_full;
+  uint64_t s_done[2];             // S_g complete (and every product issued before it)
+  uint64_t p_full[2];             // P_g written, O_g rescaled: 128 arrivals
+  uint64_t drained;               // after a failed wait: every product issued is complete
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
+               "r"(bytes), "r"(smem_addr(bar))
+               : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count));
+}
+
+// 32 columns of the thread's lane, without the wait
+__device__ __forceinline__ void tld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+// the registers of a started load, not to be used before this
+__device__ __forceinline__ void hold32(uint32_t (&r)[32]) {
+  asm volatile(
+      ""
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+        "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+        "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+        "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+__device__ __forceinline__ void tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// What a CTA has to do.
+struct AdPlace {
+  bool tail;
+  int hl, h, b, slot;
+  int n;                          // keys of the prefix or tail (below 2^23)
+  int j0, ntiles;                 // tiles of 128 keys
+  int r0, r1;                     // rows of the head (below 2^23)
+  int groups;                     // row tiles with rows: 1 or 2
+};
+__device__ __forceinline__ AdPlace ad_place(const BatchParams& p) {
+  AdPlace a;
+  const int64_t first_tail = (int64_t)p.S1 * p.tiles1 * p.Hn;
+  a.tail = blockIdx.x >= first_tail;
+  const int64_t e = a.tail ? blockIdx.x - first_tail : blockIdx.x;
+  const int S = a.tail ? p.S2 : p.S1;
+  const int64_t nb = a.tail ? p.tiles2 : p.tiles1;
+  const int range = (int)(e % S);
+  const int64_t block = e / S % nb, unit = e / S / nb;
+  a.hl = (int)(unit % p.Hn);
+  a.h = p.h0 + a.hl;
+  a.b = (int)(unit / p.Hn);
+  a.n = (int)(a.tail ? tail_length(p, a.b) : p.Nk);
+  a.slot = a.tail ? p.slot2 + range : range;
+  a.r0 = (int)((a.tail ? a.b * p.RB : 0) + block * kAdRows);
+  a.r1 = (int)(a.tail ? (a.b + 1) * p.RB : p.R);
+  a.groups = a.r1 - a.r0 > kAtTile ? 2 : 1;
+  const int64_t nt = (a.n + kAtTile - 1) / kAtTile;
+  a.j0 = (int)(nt * range / S);
+  a.ntiles = (int)(nt * (range + 1) / S) - a.j0;
+  return a;
+}
+
+__global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchParams p) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* ring = sQ + 2 * kAtOpBytes;
+  AdShared* sh = reinterpret_cast<AdShared*>(ring + kAdSlots * kAtOpBytes);
+  volatile int* abort_flag = &sh->abort_flag;
+  const AdPlace a = ad_place(p);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int ntiles = a.ntiles;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kAdSlots; ++i) { bar_init(&sh->full[i], 1); bar_init(&sh->empty[i], 1); }
+    bar_init(&sh->q_full, 1);
+    for (int g = 0; g < 2; ++g) { bar_init(&sh->s_done[g], 1); bar_init(&sh->p_full[g], kAtTile); }
+    bar_init(&sh->drained, 1);
+    sh->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh->tmem_base)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh->tmem_base;
+  const uint32_t tS = tmem, tO = tmem + 256;        // S of row tile g at column 128 g, O at 256 + 128 g
+
+  if (warp == 9) {
+    // ---------------------------------------------------------------- loader
+    if (lane == 0 && ntiles > 0) {
+      const int64_t pad = a.tail ? p.RBp : p.Rp, first = a.tail ? a.r0 - a.b * p.RB : a.r0;
+      const uint8_t* rows = p.row_img[a.tail] + (((a.tail ? (int64_t)a.b * p.Hn : 0) + a.hl) * 2 * pad + first) * 128;
+      expect_bytes(&sh->q_full, (uint32_t)(a.groups * kAtOpBytes));
+      for (int g = 0; g < a.groups; ++g)
+        for (int half = 0; half < 2; ++half)
+          bulk_load(smem_addr(sQ) + g * kAtOpBytes + half * kAtHalfBytes, rows + (half * pad + g * kAtTile) * 128, kAtHalfBytes,
+                    &sh->q_full);
+      const int64_t nt = a.tail ? p.nt2 : p.nt1;
+      const int64_t at = (((a.tail ? (int64_t)a.b * p.Hn : 0) + a.hl) * nt + a.j0) * kImageBytes;
+      const uint8_t* src[2] = {p.key_img[a.tail] + at, p.val_img[a.tail] + at};
+      int issued = 0;
+      for (int i = 0; i < 2 * ntiles; ++i) {
+        const int slot = i % kAdSlots, turn = i / kAdSlots;
+        if (turn > 0 && !bar_wait_or_abort(&sh->empty[slot], (uint32_t)((turn - 1) & 1), abort_flag)) { *abort_flag = 1; break; }
+        expect_bytes(&sh->full[slot], (uint32_t)kImageBytes);
+        bulk_load(smem_addr(ring) + slot * kAtOpBytes, src[i & 1] + (int64_t)(i >> 1) * kImageBytes, (uint32_t)kImageBytes,
+                  &sh->full[slot]);
+        ++issued;
+      }
+      // no copy may be in flight when the CTA leaves
+      bar_wait(&sh->q_full, 0);
+      for (int i = issued > kAdSlots ? issued - kAdSlots : 0; i < issued; ++i)
+        bar_wait(&sh->full[i % kAdSlots], (uint32_t)((i / kAdSlots) & 1));
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- issuer
+    if (lane == 0 && ntiles > 0) {
+      bool ok = bar_wait_or_abort(&sh->q_full, 0, abort_flag);
+      auto wait_full = [&](int i) {
+        return bar_wait_or_abort(&sh->full[i % kAdSlots], (uint32_t)((i / kAdSlots) & 1), abort_flag);
+      };
+      auto scores = [&](int g, int j) {
+        const uint32_t a0 = smem_addr(sQ + g * kAtOpBytes), b0 = smem_addr(ring) + (2 * j % kAdSlots) * kAtOpBytes;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma(tS + 128 * g, op_desc_k(a0, kk), op_desc_k(b0, kk), kk > 0 ? 1u : 0u);
+      };
+      ok = ok && wait_full(0);
+      if (ok) {
+        fence_after();
+        for (int g = 0; g < a.groups; ++g) { scores(g, 0); mma_commit(&sh->s_done[g]); }
+        mma_commit(&sh->empty[0]);
+      }
+      for (int j = 0; ok && j < ntiles; ++j) {
+        const int iv = 2 * j + 1, ik = 2 * j + 2;
+        const bool more = j + 1 < ntiles;
+        ok = wait_full(iv);
+        for (int g = 0; ok && g < a.groups; ++g) {
+          ok = bar_wait_or_abort(&sh->p_full[g], (uint32_t)(j & 1), abort_flag);
+          if (!ok) break;
+          fence_after();
+          const uint32_t b0 = smem_addr(ring) + (iv % kAdSlots) * kAtOpBytes;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ta(tO + 128 * g, tS + 128 * g + (uint32_t)(8 * kk), op_desc_k(b0, kk), (j > 0 || kk > 0) ? 1u : 0u);
+          if (g == a.groups - 1) mma_commit(&sh->empty[iv % kAdSlots]);
+          if (more) {
+            if (g == 0) ok = wait_full(ik);
+            if (!ok) break;
+            fence_after();
+            scores(g, j + 1);
+          }
+          mma_commit(&sh->s_done[g]);                  // the last one: O_g is complete
+          if (more && g == a.groups - 1) mma_commit(&sh->empty[ik % kAdSlots]);
+        }
+      }
+      if (!ok) {
+        *abort_flag = 1;
+        // let the products that were issued finish (bounded) before the tensor memory is freed
+        mma_commit(&sh->drained);
+        bar_wait(&sh->drained, 0);
+      }
+    }
+  } else if ((warp >> 2) < a.groups) {
+    // ---------------------------------------------------------------- softmax of row tile g
+    const int g = warp >> 2, qi = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+    const uint32_t tSt = tS + 128 * g + lane_base, tOt = tO + 128 * g + lane_base;
+    const int row = a.r0 + g * kAtTile + qi;
+    const int limit = row < a.r1 ? row_limit(p, query_pos(p, row)) : kLimitNone;
+    // the least limit of the warp's live rows
+    const int least = __reduce_min_sync(0xffffffffu, limit != kLimitNone ? limit : kPosNever);
+    const bool in_order = !a.tail && p.k_pos == nullptr;
+    float m_run = kNoMax, l_run = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < ntiles; ++j) {
+      // Does any live row of the warp miss a key of this tile?  Where positions
+      // are in order the last one tells; otherwise the lanes look at four each.
+      const int k0 = (a.j0 + j) * kAtTile, valid = min(a.n - k0, kAtTile);
+      bool masked = valid < kAtTile || (p.causal && in_order && k0 + valid - 1 > least);
+      int kp[4];
+      if (masked || (p.causal && !in_order)) {
+        bool over = false;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          kp[c] = mask_pos(p, a.tail, a.h, a.b, k0 + 32 * c + lane, a.n);
+          over |= kp[c] > least;
+        }
+        masked = __any_sync(0xffffffffu, over);
+      }
+      ok = bar_wait_or_abort(&sh->s_done[g], (uint32_t)(j & 1), abort_flag);
+      if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+      fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tld32_start(tSt + 32 * c, s[c]);
+      tld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) hold32(s[c]);
+      if (masked) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (__shfl_sync(0xffffffffu, kp[c], e) > limit) s[c][e] = 0xFF800000u;       // -inf
+      }
+      float mx[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+        for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+      }
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl;
+      const float m_new = mt > m_run + 8.0f ? mt : m_run;
+      const float alpha = exp2_approx(m_run - m_new);
+      const float2 sl2 = make_float2(p.sl, p.sl), nm2 = make_float2(-m_new, -m_new);
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sl2, nm2);
+          w[e] = pack_bf16(exp2_approx(x.x), exp2_approx(x.y));
+          // the sum of the rounded weights, the ones the product uses
+          sum[e & 1] = __fadd2_rn(sum[e & 1], make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)));
+        }
+        tst16(tSt + 16 * c, w);
+      }
+      l_run = l_run * alpha + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
+      m_run = m_new;
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {           // rescale O_g
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t rg[16];
+          tld16(tOt + 16 * c, rg);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) rg[e] = __float_as_uint(__uint_as_float(rg[e]) * alpha);
+          tst16(tOt + 16 * c, rg);
+        }
+      }
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      fence_before();
+      mbar_arrive(&sh->p_full[g]);
+    }
+    if (ok && ntiles > 0) {
+      ok = bar_wait_or_abort(&sh->s_done[g], (uint32_t)(ntiles & 1), abort_flag);
+      ok = !__any_sync(0xffffffffu, !ok);
+      fence_after();
+    }
+    if (!ok) *abort_flag = 1;
+    if (ok) {
+      const bool whole = p.slots == 1;                 // nothing to join: O itself
+      const bool dead = limit == kLimitNone || l_run == 0.0f;
+      const int64_t out = ((int64_t)a.slot * p.H + a.h) * p.R + row;
+      if (row < a.r1 && !whole) p.part_ml[out] = make_float2(m_run, dead ? 0.0f : l_run);
+      const float inv = dead ? 0.0f : 1.0f / l_run;
+      if (ntiles > 0) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t rg[32];
+          tld32(tOt + 32 * c, rg);
+          if (row >= a.r1) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(p.O + query_row(p, a.h, row) * kD + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float x = __uint_as_float(rg[8 * e + 2 * i]), y = __uint_as_float(rg[8 * e + 2 * i + 1]);
+                w[i] = dead ? 0u : pack_bf16(x * inv, y * inv);
+              }
+              dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          } else {
+            float4* dst = reinterpret_cast<float4*>(p.part_O + out * kD + 32 * c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              dst[e] = make_float4(__uint_as_float(rg[4 * e]), __uint_as_float(rg[4 * e + 1]),
+                                   __uint_as_float(rg[4 * e + 2]), __uint_as_float(rg[4 * e + 3]));
+          }
+        }
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, 1u);
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+size_t ad_smem_bytes() { return 1024 + (size_t)(2 + kAdSlots) * kAtOpBytes + sizeof(AdShared); }
+
+}  // namespace
+
+cudaError_t launch_batch_attend(const BatchParams& p, cudaStream_t s) {
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(qvg_batch_attend), ad_smem_bytes());
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)(p.S1 * p.tiles1 * p.Hn + p.S2 * p.tiles2 * p.Hn * p.B);
+  qvg_batch_attend<<<grid, kAdThreads, ad_smem_bytes(), s>>>(p);
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- plans
+namespace {
+
+constexpr int kRowTile = 16;                      // rows and keys of a step of the kernels for few rows
+constexpr int kRowStep = 64;
+constexpr int64_t kManyRows = 48;                 // rows beyond which tcgen05 takes over
+constexpr size_t kImageBudget = size_t(1) << 30;  // operand tiles in the workspace at a time, about
+
+BatchParams params_of(const BatchArgs& a) {
+  BatchParams p{};
+  for (int w = 0; w < 2; ++w) {
+    const qvg_packed* pk = w == 0 ? a.k : a.v;
+    if (pk == nullptr) continue;
+    p.codes[w] = pk->codes; p.scale[w] = pk->scale; p.zero[w] = pk->zero; p.assign[w] = pk->assign;
+    p.tab[w] = static_cast<const __nv_bfloat16*>(pk->centroids);
+  }
+  const qvg_batch& q = *a.batch;
+  p.Q = static_cast<const __nv_bfloat16*>(q.Q);
+  p.q_pos = q.q_pos;
+  p.k_pos = q.k_pos;
+  p.tail[0] = static_cast<const __nv_bfloat16*>(q.tail_k);
+  p.tail[1] = static_cast<const __nv_bfloat16*>(q.tail_v);
+  p.tail_pos = q.tail_pos;
+  p.tail_len = q.tail_len;
+  p.rope = reinterpret_cast<const float2*>(static_cast<const char*>(a.tables) + kRopeHeaderBytes);
+  p.status = static_cast<uint32_t*>(const_cast<void*>(a.tables));
+  p.max_pos = a.max_pos;
+  p.Nk = a.Nk; p.Nq = q.Nq; p.Nt = q.Nt;
+  p.RB = q.group * q.Nq;
+  p.R = q.B * p.RB;
+  p.B = q.B; p.H = a.H; p.K = a.K; p.T = a.T; p.G = a.G; p.sym = a.sym; p.causal = q.causal;
+  for (int g = a.G; g > 1; g >>= 1) ++p.lgG;
+  p.sl = 1.4426950408889634f / sqrtf((float)kD);
+  p.nt1 = (p.Nk + kAtTile - 1) / kAtTile;
+  p.nt2 = (p.Nt + kAtTile - 1) / kAtTile;
+  p.Rp = (p.R + kAdRows - 1) / kAdRows * kAdRows;
+  p.RBp = (p.RB + kAdRows - 1) / kAdRows * kAdRows;
+  return p;
+}
+
+// Which kernels run, over which ranges, and what they need of the workspace.
+// The prefix goes to the tensor-core kernels when a head has many rows, a tail
+// when a sequence has.
+struct BatchPlan {
+  bool tc1, tc2;                  // prefix, tails
+  int S1, S2, Hn;
+  size_t bytes;
+};
+
+// Places everything in the workspace at `ws` (null: sizes only) and returns
+// its length.
+size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    char* r = ws != nullptr ? ws + at : nullptr;
+    at += (n + 255) & ~size_t(255);
+    return r;
+  };
+  p.slots = plan.S1 + plan.S2;
+  p.slot2 = plan.S1;
+  const size_t rows = (size_t)p.H * p.R;
+  if (values) p.part_O = reinterpret_cast<float*>(take(p.slots > 1 || !plan.tc1 ? p.slots * rows * kD * sizeof(float) : 0));
+  p.part_ml = reinterpret_cast<float2*>(take(p.slots * rows * sizeof(float2)));
+  if (plan.tc1) {
+    p.key_img[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.nt1 * kImageBytes));
+    p.val_img[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.nt1 * kImageBytes));
+    p.row_img[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.Rp * kD * 2));
+    if (!values) p.row_lo[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.Rp * kD * 2));
+  }
+  if (plan.tc2) {
+    p.key_img[1] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.B * p.nt2 * kImageBytes));
+    p.val_img[1] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.B * p.nt2 * kImageBytes));
+    p.row_img[1] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.B * p.RBp * kD * 2));
+    if (!values) p.row_lo[1] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.B * p.RBp * kD * 2));
+  }
+  return at;
+}
+
+// The cut of the keys.  For few rows: enough CTAs to fill the SMs four times
+// over, at least one step of keys to each.  For many: the plan with the least
+// estimated time, in key tiles of a CTA that holds an SM: a CTA of t tiles
+// takes t + 3 (its start and its end), the tails' CTAs fill the gaps of the
+// prefix's last wave first, and a range's partial results cost their way
+// through memory (about a fifth of a tile per CTA's worth of rows and range).
+BatchPlan plan_batch(BatchParams& p, bool values) {
+  BatchPlan plan{};
+  const double sms = (double)device_sm_count();
+  plan.tc1 = values && p.R > kManyRows;
+  plan.tc2 = plan.tc1 && p.Nt > 0 && p.RB > kManyRows;
+  plan.Hn = p.H;
+  if (!plan.tc1) {
+    const int64_t units = (p.R + kRowTile - 1) / kRowTile * p.H;
+    const int64_t most1 = (p.Nk + kRowStep - 1) / kRowStep;
+    plan.S1 = (int)std::max<int64_t>(1, std::min<int64_t>({((int64_t)(4 * sms) + units - 1) / units, most1, 64}));
+  }
+  if (p.Nt > 0 && !plan.tc2) {
+    const int64_t units = (p.RB + kRowTile - 1) / kRowTile * p.H * p.B;
+    const int64_t most2 = (p.Nt + kRowStep - 1) / kRowStep;
+    plan.S2 = (int)std::max<int64_t>(1, std::min<int64_t>({((int64_t)(4 * sms) + units - 1) / units, most2, 8}));
+  }
+  if (plan.tc1) {
+    size_t per_head = (size_t)p.nt1 * 2 * kImageBytes;
+    if (plan.tc2) per_head += (size_t)p.B * p.nt2 * 2 * kImageBytes;
+    plan.Hn = (int)std::max<int64_t>(1, std::min<int64_t>(p.H, (int64_t)(kImageBudget / per_head)));
+    const int64_t u1 = (p.Rp / kAdRows) * plan.Hn, u2 = plan.tc2 ? (p.RBp / kAdRows) * plan.Hn * p.B : 0;
+    double best = -1.0;
+    for (int64_t s1 = 1; s1 <= std::min<int64_t>(p.nt1, kAdMaxRanges); ++s1) {
+      const double t1 = (double)((p.nt1 + s1 - 1) / s1) + 3.0;
+      const int64_t s2 = u2 > 0 ? std::max<int64_t>(1, std::min<int64_t>(p.nt2, (int64_t)((double)p.nt2 / t1 + 0.5))) : 0;
+      const double t2 = s2 > 0 ? (double)((p.nt2 + s2 - 1) / s2) + 3.0 : 0.0;
+      const double waves = std::ceil((double)(u1 * s1) / sms);
+      double cost = waves * t1;
+      const double gaps = (waves * sms - (double)(u1 * s1)) * t1, rest = (double)(u2 * s2) * t2 - 0.8 * gaps;
+      if (rest > 0.0) cost += std::max(t2, rest / sms + 0.5 * t2);
+      if (s1 + s2 + (plan.tc2 ? 0 : plan.S2) > 1) cost += 2.0 + 0.2 * (double)(s1 + s2) * (double)u1 / sms;
+      if (best < 0.0 || cost < best) {
+        best = cost;
+        plan.S1 = (int)s1;
+        if (plan.tc2) plan.S2 = (int)s2;
+      }
+    }
+  }
+  plan.bytes = place(p, plan, values, nullptr);
+  return plan;
+}
+
+// The launch's share of the plan: what the kernels for few rows take, or the
+// tensor-core kernels.
+BatchParams share(const BatchParams& p, const BatchPlan& plan, bool tc) {
+  BatchParams q = p;
+  q.S1 = plan.tc1 == tc ? plan.S1 : 0;
+  q.S2 = plan.tc2 == tc ? plan.S2 : 0;
+  const int64_t tile = tc ? kAdRows : kRowTile;
+  q.tiles1 = (p.R + tile - 1) / tile;
+  q.tiles2 = (p.RB + tile - 1) / tile;
+  return q;
+}
+
+}  // namespace
+
+size_t attention_batch_workspace_bytes(const BatchArgs& a) {
+  BatchParams p = params_of(a);
+  return plan_batch(p, true).bytes;
+}
+
+size_t attention_weights_workspace_bytes(const BatchArgs& a) {
+  BatchParams p = params_of(a);
+  return plan_batch(p, false).bytes;
+}
+
+cudaError_t launch_attention_batch(const BatchArgs& a, void* O, void* ws, cudaStream_t s) {
+  BatchParams p = params_of(a);
+  const BatchPlan plan = plan_batch(p, true);
+  place(p, plan, true, static_cast<char*>(ws));
+  p.O = static_cast<__nv_bfloat16*>(O);
+  cudaError_t e = cudaSuccess;
+  const BatchParams few = share(p, plan, false);
+  if (few.S1 + few.S2 > 0 && (e = launch_rows_partial(few, true, s)) != cudaSuccess) return e;
+  if (plan.tc1) {
+    BatchParams q = share(p, plan, true);
+    for (q.h0 = 0; q.h0 < p.H; q.h0 += plan.Hn) {
+      q.Hn = std::min(plan.Hn, p.H - q.h0);
+      if ((e = launch_batch_expand(q, false, s)) != cudaSuccess) return e;
+      if ((e = launch_batch_attend(q, s)) != cudaSuccess) return e;
+    }
+    if (p.slots == 1) return e;
+  }
+  return launch_batch_merge(p, s);
+}
+
+cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, float* out, void* ws, cudaStream_t s) {
+  BatchParams p = params_of(a);
+  const BatchPlan plan = plan_batch(p, false);
+  place(p, plan, false, static_cast<char*>(ws));
+  const BatchParams few = share(p, plan, false);
+  const cudaError_t e = launch_rows_partial(few, false, s);
+  if (e != cudaSuccess) return e;
+  return launch_rows_weights(p, received, out, s);
+}
+
+}  // namespace qvg

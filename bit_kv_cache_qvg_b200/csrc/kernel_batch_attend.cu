@@ -55,6 +55,29 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count));
 }
 
+// B operand of O += P V: V's image holds a key's 64 channels of a half in 128
+// bytes, so B is N-major: 64 channels to the swizzled row, the other half
+// LBO = 16 KB on, 8 keys to the 1,024-byte group (SBO).  K-step kk takes keys
+// 16 kk .. 16 kk + 15.
+__device__ __forceinline__ uint64_t value_desc(uint32_t saddr, int kk) {
+  uint64_t d = 0;
+  d |= (uint64_t)(((saddr + (uint32_t)kk * 2048u) >> 4) & 0x3FFF);
+  d |= (uint64_t)(kAtHalfBytes >> 4) << 16;     // LBO
+  d |= (uint64_t)(1024 >> 4) << 32;             // SBO
+  d |= (uint64_t)1 << 46;                       // version
+  d |= (uint64_t)2 << 61;                       // SWIZZLE_128B
+  return d;
+}
+// D += A B with A (P, bf16) in tensor memory and B N-major
+__device__ __forceinline__ void mma_values(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(kIdesc | (1u << 16)), "r"(accumulate)
+      : "memory");
+}
+
 // 32 columns of the thread's lane, without the wait
 __device__ __forceinline__ void tld32_start(uint32_t taddr, uint32_t (&r)[32]) {
   asm volatile(
@@ -197,7 +220,7 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
           const uint32_t b0 = smem_addr(ring) + (iv % kAdSlots) * kAtOpBytes;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ta(tO + 128 * g, tS + 128 * g + (uint32_t)(8 * kk), op_desc_k(b0, kk), (j > 0 || kk > 0) ? 1u : 0u);
+            mma_values(tO + 128 * g, tS + 128 * g + (uint32_t)(8 * kk), value_desc(b0, kk), (j > 0 || kk > 0) ? 1u : 0u);
           if (g == a.groups - 1) mma_commit(&sh->empty[iv % kAdSlots]);
           if (more) {
             if (g == 0) ok = wait_full(ik);

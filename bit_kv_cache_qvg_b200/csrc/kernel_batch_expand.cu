@@ -2,16 +2,19 @@
 // qvg_attention_weights for many rows, written once for all of them.
 //
 // The attention kernels read a key tile once for every 256 rows.  With more
-// rows than that, rebuilding it each time costs more than the products: the
-// rebuilding kernel of qvg_attention, over the rows of a batch, took 2.58 ms
+// rows than that, rebuilding it each time costs more than the products: a
+// kernel that rebuilt the tiles on the fly, as qvg_attention does, took 2.58 ms
 // for 1,520 rows over 38,000 tokens of 32 heads.  So a tile is rebuilt once,
 // into the workspace, as the 32 KB image that a bulk copy brings into shared
-// memory as it is: bf16, K-major, 128-byte swizzle (attention_tc.cuh), keys by
-// channels for K and channels by keys for V.  The rows are rotated once, too.
+// memory as it is: 128 keys x 128 channels in bf16, two halves of 64 channels,
+// a key's 128 bytes of a half swizzled by key mod 8 (attention_tc.cuh).  K is
+// the K-major operand of S = Q K'^T in this layout and V the N-major one of
+// O = P V.  The rows are rotated once, too.
 //
-// One CTA builds one tile (128 keys of K and V, or the high and low halves of
-// K) in shared memory and stores it with bulk copies; bound by the 512 bytes
-// written a token.
+// Eight lanes take a key, two 8-channel chunks each (c and c + 8), so a warp
+// reads 128 contiguous bytes of a centroid row and writes 128 of an image.  The
+// work is arithmetic on 16 values a lane; the bound is the 512 bytes written a
+// token.
 #include "attention_tc.cuh"
 #include "batch.cuh"
 
@@ -19,33 +22,31 @@ namespace qvg {
 namespace {
 
 constexpr int kExThreads = 256;
+constexpr int kExKeys = kExThreads / 8;           // keys per pass
+constexpr int kExPasses = kAtTile / kExKeys;
 
-__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
-}
-
-// u + iw = (a + ib) e^(i phi): high halves, and (precise) what their rounding left
-__device__ __forceinline__ void turn_pair(uint32_t x, float c, float s, bool precise, uint32_t& hi, uint32_t& lo) {
+// (a + ib) e^(i phi) of a pair of channels: high halves, and (PRECISE) what
+// their rounding left
+template <bool PRECISE>
+__device__ __forceinline__ void turn_pair(uint32_t x, float c, float s, uint32_t& hi, uint32_t& lo) {
   const float a = lo_f(x), b = hi_f(x);
-  const float u = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)), w = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+  const float u = fmaf(a, c, -(b * s)), w = fmaf(a, s, b * c);
   hi = pack2(u, w);
-  lo = precise ? pack2(u - lo_f(hi), w - hi_f(hi)) : 0u;
+  if (PRECISE) lo = pack2(u - lo_f(hi), w - hi_f(hi));
 }
-__device__ __forceinline__ void turn_chunk(const BatchParams& p, uint4 x, int64_t pos, int c0, bool precise, uint4& hi, uint4& lo) {
-  const float4* cs4 = reinterpret_cast<const float4*>(p.rope + rope_row(p, pos) * (kD / 2) + c0 / 2);
-  const float4 t0 = __ldg(cs4), t1 = __ldg(cs4 + 1);
-  turn_pair(x.x, t0.x, t0.y, precise, hi.x, lo.x);
-  turn_pair(x.y, t0.z, t0.w, precise, hi.y, lo.y);
-  turn_pair(x.z, t1.x, t1.y, precise, hi.z, lo.z);
-  turn_pair(x.w, t1.z, t1.w, precise, hi.w, lo.w);
-}
-__device__ __forceinline__ uint4 pack_row(const float (&y)[8]) {
-  return make_uint4(pack2(y[0], y[1]), pack2(y[2], y[3]), pack2(y[4], y[5]), pack2(y[6], y[7]));
+template <bool PRECISE>
+__device__ __forceinline__ void turn_chunk(const float4* cs, uint4 x, uint4& hi, uint4& lo) {
+  const float4 t0 = __ldg(cs), t1 = __ldg(cs + 1);
+  turn_pair<PRECISE>(x.x, t0.x, t0.y, hi.x, lo.x);
+  turn_pair<PRECISE>(x.y, t0.z, t0.w, hi.y, lo.y);
+  turn_pair<PRECISE>(x.z, t1.x, t1.y, hi.z, lo.z);
+  turn_pair<PRECISE>(x.w, t1.z, t1.w, hi.w, lo.w);
 }
 
-// 128 rows of a head (r0 in the head's rows) or of one sequence, rotated at
-// their positions; zeros behind the last one.
-__device__ __forceinline__ void expand_rows(const BatchParams& p, bool by_sequence, int hl, int b, int64_t tile, bool precise) {
+// 128 rows of a head, or of one sequence, rotated at their positions; zeros
+// behind the last one.
+template <bool PRECISE>
+__device__ __forceinline__ void expand_rows(const BatchParams& p, bool by_sequence, int hl, int b, int64_t tile) {
   const int which = by_sequence ? 1 : 0;
   const int64_t rows = by_sequence ? p.RB : p.R, pad = by_sequence ? p.RBp : p.Rp;
   const int64_t base = ((by_sequence ? (int64_t)b * p.Hn : 0) + hl) * 2 * pad;
@@ -56,39 +57,170 @@ __device__ __forceinline__ void expand_rows(const BatchParams& p, bool by_sequen
     if (r < rows) {
       const int64_t row = by_sequence ? b * p.RB + r : r;
       const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.Q + query_row(p, p.h0 + hl, row) * kD + 8 * cb));
-      turn_chunk(p, x, query_pos(p, row), 8 * cb, precise, hi, lo);
+      turn_chunk<PRECISE>(reinterpret_cast<const float4*>(p.rope + rope_row(p, query_pos(p, row)) * (kD / 2) + 4 * cb), x, hi, lo);
     }
     const int64_t at = (base + (cb >> 3) * pad + r) * 128 + (((cb & 7) ^ (int)(r & 7)) << 4);
     *reinterpret_cast<uint4*>(p.row_img[which] + at) = hi;
-    if (precise) *reinterpret_cast<uint4*>(p.row_lo[which] + at) = lo;
+    if (PRECISE) *reinterpret_cast<uint4*>(p.row_lo[which] + at) = lo;
   }
 }
 
-// CTAs: the prefix's key tiles, the tails', the rows by head, the rows by
-// sequence.  PRECISE: the second image of a tile holds the keys' low halves
-// instead of the values.
+// The reconstructed chunks c and c + 8 of a prefix token as packed bf16 pairs
+// (the arithmetic of qvg_dequant_fused).  The pointers are the head's; offsets
+// within a head fit in 32 bits.
+template <int TT>
+struct Rebuild {
+  const uint8_t *codes, *scale, *zero, *assign;
+  const __nv_bfloat16* tab;
+  int64_t assign_stage, tab_stage;
+  uint32_t top;                   // K - 1
+  int lgng, g0, g1, sym, T;       // log2(d/G), the chunks' groups
+
+  __device__ __forceinline__ Rebuild(const BatchParams& p, int w, int h, int c) {
+    lgng = 7 - p.lgG;
+    const int64_t row = (int64_t)h * p.Nk;
+    codes = p.codes[w] + row * (kD / 4) + 2 * c;
+    scale = p.scale[w] + (row << lgng);
+    zero = p.zero[w] + (p.sym ? 0 : (row << lgng));
+    assign = p.assign[w] + row;
+    tab = p.tab[w] + (int64_t)h * p.K * kD + 8 * c;
+    assign_stage = (int64_t)p.H * p.Nk;
+    tab_stage = (int64_t)p.H * p.K * kD;
+    top = (uint32_t)p.K - 1;
+    g0 = (8 * c) >> p.lgG;
+    g1 = (64 + 8 * c) >> p.lgG;
+    sym = p.sym;
+    T = TT >= 0 ? TT : p.T;
+  }
+  __device__ __forceinline__ void operator()(const float2* nlut, uint32_t tok, uint4 (&out)[2]) const {
+    const uint32_t code[2] = {__ldg(reinterpret_cast<const uint16_t*>(codes + tok * 32u)),
+                              __ldg(reinterpret_cast<const uint16_t*>(codes + tok * 32u + 16u))};
+    const uint32_t at = tok << lgng;
+    uint32_t sz[2] = {__ldg(scale + at + g0), __ldg(scale + at + g1)};
+    if (!sym) {
+      sz[0] |= (uint32_t)__ldg(zero + at + g0) << 8;
+      sz[1] |= (uint32_t)__ldg(zero + at + g1) << 8;
+    }
+    constexpr int TR = TT > 0 ? TT : 1;
+    uint4 rows[TR][2];
+    if (TT > 0) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const uint32_t k = min((uint32_t)__ldg(assign + t * assign_stage + tok), top);
+        const uint4* row = reinterpret_cast<const uint4*>(tab + t * tab_stage + k * (uint32_t)kD);
+        rows[t][0] = __ldg(row);
+        rows[t][1] = __ldg(row + 8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float2 sm = e4m3_pair(sz[i]);
+      const float2 s2 = make_float2(sm.x, sm.x), m2 = make_float2(sm.y, sm.y);
+      float2 y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 q = nlut[(code[i] >> (4 * e)) & 0xFu];
+        y[e] = sym ? __fmul2_rn(s2, q) : __ffma2_rn(s2, q, m2);
+      }
+      auto add = [&](const uint4& v) {
+        y[0] = __fadd2_rn(y[0], make_float2(lo_f(v.x), hi_f(v.x)));
+        y[1] = __fadd2_rn(y[1], make_float2(lo_f(v.y), hi_f(v.y)));
+        y[2] = __fadd2_rn(y[2], make_float2(lo_f(v.z), hi_f(v.z)));
+        y[3] = __fadd2_rn(y[3], make_float2(lo_f(v.w), hi_f(v.w)));
+      };
+      if (TT > 0) {
+#pragma unroll
+        for (int t = TT - 1; t >= 0; --t) add(rows[t][i]);
+      } else if (TT < 0) {
+        for (int t = T - 1; t >= 0; --t) {
+          const uint32_t k = min((uint32_t)__ldg(assign + t * assign_stage + tok), top);
+          add(__ldg(reinterpret_cast<const uint4*>(tab + t * tab_stage + k * (uint32_t)kD) + 8 * i));
+        }
+      }
+      out[i] = make_uint4(pack2(y[0].x, y[0].y), pack2(y[1].x, y[1].y), pack2(y[2].x, y[2].y), pack2(y[3].x, y[3].y));
+    }
+  }
+};
+
+// One tile of K (rotated; PRECISE: and its low halves) or of V.
+template <int TT, bool KEYS, bool PRECISE>
+__device__ __forceinline__ void expand_tile(const BatchParams& p, const float2* nlut, bool tail, int h, int b, int tile0, int n,
+                                            uint8_t* img, uint8_t* img_lo) {
+  const int c = threadIdx.x & 7, key0 = threadIdx.x >> 3;
+  // a lane's place in the image does not depend on the pass: 32 keys on, the swizzle is the same
+  const uint32_t place = (uint32_t)(key0 * 128 + ((c ^ (key0 & 7)) << 4));
+  auto put = [&](int pass, int key, uint4 (&x)[2]) {
+    uint8_t* dst = img + place + pass * (kExKeys * 128);
+    if (!KEYS) {
+      *reinterpret_cast<uint4*>(dst) = x[0];
+      *reinterpret_cast<uint4*>(dst + kAtHalfBytes) = x[1];
+      return;
+    }
+    int64_t pos = key;
+    if (tail || p.k_pos != nullptr) pos = rope_row(p, raw_key_pos(p, tail, h, b, key));
+    const float4* cs = reinterpret_cast<const float4*>(p.rope + pos * (kD / 2) + 4 * c);
+    uint4 hi[2], lo[2];
+    turn_chunk<PRECISE>(cs, x[0], hi[0], lo[0]);
+    turn_chunk<PRECISE>(cs + 16, x[1], hi[1], lo[1]);
+    *reinterpret_cast<uint4*>(dst) = hi[0];
+    *reinterpret_cast<uint4*>(dst + kAtHalfBytes) = hi[1];
+    if (PRECISE) {
+      uint8_t* dl = img_lo + place + pass * (kExKeys * 128);
+      *reinterpret_cast<uint4*>(dl) = lo[0];
+      *reinterpret_cast<uint4*>(dl + kAtHalfBytes) = lo[1];
+    }
+  };
+  if (!tail) {
+    const Rebuild<TT> rebuild(p, KEYS ? 0 : 1, h, c);
+#pragma unroll 2
+    for (int pass = 0; pass < kExPasses; ++pass) {
+      const int key = min(tile0 + pass * kExKeys + key0, n - 1);     // past the end: the last token, finite and not used
+      uint4 x[2];
+      rebuild(nlut, (uint32_t)key, x);
+      put(pass, key, x);
+    }
+  } else {
+    // a tail's tokens are bf16 rows already; behind its length zeros
+    const __nv_bfloat16* rows = p.tail[KEYS ? 0 : 1] + ((int64_t)b * p.H + h) * p.Nt * kD + 8 * c;
+#pragma unroll 2
+    for (int pass = 0; pass < kExPasses; ++pass) {
+      const int key = tile0 + pass * kExKeys + key0;
+      uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+      if (key < n) {
+        const uint4* row = reinterpret_cast<const uint4*>(rows + (int64_t)key * kD);
+        x[0] = __ldg(row);
+        x[1] = __ldg(row + 8);
+      }
+      put(pass, min(key, n - 1), x);
+    }
+  }
+}
+
+// CTAs: the prefix's tiles (K, then V unless PRECISE, of every key tile), the
+// tails', the rows by head, the rows by sequence.  PRECISE: the second image
+// of a tile holds the keys' low halves instead of the values.
 template <int TT, bool PRECISE>
-__global__ void __launch_bounds__(kExThreads, 3) qvg_batch_expand(const BatchParams p, const int64_t tiles_p, const int64_t tiles_t,
-                                                                 const int64_t row_tiles) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sK = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sV = sK + kImageBytes;
+__global__ void __launch_bounds__(kExThreads) qvg_batch_expand(const BatchParams p, const int64_t tiles_p, const int64_t tiles_t,
+                                                              const int64_t row_tiles) {
   __shared__ float2 nlut[16];
+  constexpr int kKinds = PRECISE ? 1 : 2;
   int64_t id = blockIdx.x;
-  if (id >= tiles_p + tiles_t) {
-    id -= tiles_p + tiles_t;
+  if (id >= kKinds * (tiles_p + tiles_t)) {
+    id -= kKinds * (tiles_p + tiles_t);
     const bool by_sequence = id >= row_tiles;
     if (by_sequence) id -= row_tiles;
     const int64_t per = (by_sequence ? p.RBp : p.Rp) / 128;
     const int64_t unit = id / per;
-    expand_rows(p, by_sequence, (int)(unit % p.Hn), (int)(unit / p.Hn), id % per, PRECISE);
+    expand_rows<PRECISE>(p, by_sequence, (int)(unit % p.Hn), (int)(unit / p.Hn), id % per);
     return;
   }
+  const bool values = !PRECISE && (id & 1) != 0;
+  if (!PRECISE) id >>= 1;
   const bool tail = id >= tiles_p;
   if (tail) id -= tiles_p;
   const int64_t nt = tail ? p.nt2 : p.nt1, unit = id / nt;
   const int j = (int)(id % nt), hl = (int)(unit % p.Hn), b = (int)(unit / p.Hn), h = p.h0 + hl;
-  const int64_t n = tail ? tail_length(p, b) : p.Nk;
+  const int n = (int)(tail ? tail_length(p, b) : p.Nk);
   const int tile0 = j * kAtTile;
   if (tile0 >= n) return;                          // a tail's tile that nobody reads
   if (threadIdx.x < 16) {
@@ -96,72 +228,9 @@ __global__ void __launch_bounds__(kExThreads, 3) qvg_batch_expand(const BatchPar
     nlut[threadIdx.x] = make_float2((float)(threadIdx.x & 3u) - off, (float)(threadIdx.x >> 2) - off);
   }
   __syncthreads();
-  const int r = threadIdx.x;
-  const int rb = r >> 4, cb = r & 15;              // K: rows 32 s + 2 rb, + 1, channels 8 cb ..
-  const int rbv = r & 31, cbv = r >> 5;            // V: keys 64 (s & 1) + 2 rbv, + 1, channels 8 (cbv + 8 (s >> 1)) ..
-  auto put_k = [&](int row, uint4 x, int64_t pos) {
-    uint4 hi, lo;
-    turn_chunk(p, x, pos, 8 * cb, PRECISE, hi, lo);
-    *reinterpret_cast<uint4*>(sK + op_off(row, 8 * cb)) = hi;
-    if (PRECISE) *reinterpret_cast<uint4*>(sV + op_off(row, 8 * cb)) = lo;
-  };
-  if (!tail) {
-#pragma unroll 1
-    for (int s = 0; s < 4; ++s) {
-      ReconBlock<TT, 2, BatchParams> bk, bv;
-      const int rk = 32 * s + 2 * rb, rv = 64 * (s & 1) + 2 * rbv, cv = 8 * (cbv + 8 * (s >> 1));
-      bk.load_tokens(p, 0, h, tile0 + rk, 8 * cb);
-      if (!PRECISE) bv.load_tokens(p, 1, h, tile0 + rv, cv);
-      bk.load_rows(p, h);
-      if (!PRECISE) bv.load_rows(p, h);
-      float y[2][8];
-      bk.finish(p, nlut, h, y);
-#pragma unroll
-      for (int rr = 0; rr < 2; ++rr) {
-        const int64_t key = tile0 + rk + rr < n ? tile0 + rk + rr : n - 1;
-        put_k(rk + rr, pack_row(y[rr]), raw_key_pos(p, false, h, 0, key));
-      }
-      if (!PRECISE) {
-        bv.finish(p, nlut, h, y);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) *reinterpret_cast<uint32_t*>(sV + op_off(cv + e, rv)) = pack2(y[0][e], y[1][e]);
-      }
-    }
-  } else {
-    // a tail's tokens are bf16 rows already; behind its length zeros
-    const int64_t base = ((int64_t)b * p.H + h) * p.Nt;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int rk = 32 * s + 2 * rb, rv = 64 * (s & 1) + 2 * rbv, cv = 8 * (cbv + 8 * (s >> 1));
-      uint4 v[2];
-#pragma unroll
-      for (int rr = 0; rr < 2; ++rr) {
-        const int64_t key = tile0 + rk + rr, val = tile0 + rv + rr;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        v[rr] = x;
-        if (key < n) x = __ldg(reinterpret_cast<const uint4*>(p.tail[0] + (base + key) * kD + 8 * cb));
-        put_k(rk + rr, x, key < n ? raw_key_pos(p, true, h, b, key) : 0);
-        if (!PRECISE && val < n) v[rr] = __ldg(reinterpret_cast<const uint4*>(p.tail[1] + (base + val) * kD + cv));
-      }
-      if (!PRECISE) {
-        const uint32_t x0[4] = {v[0].x, v[0].y, v[0].z, v[0].w}, x1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          *reinterpret_cast<uint32_t*>(sV + op_off(cv + 2 * e, rv)) = __byte_perm(x0[e], x1[e], 0x5410);
-          *reinterpret_cast<uint32_t*>(sV + op_off(cv + 2 * e + 1, rv)) = __byte_perm(x0[e], x1[e], 0x7632);
-        }
-      }
-    }
-  }
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const int64_t at = (((tail ? (int64_t)b * p.Hn : 0) + hl) * nt + j) * kImageBytes;
-    bulk_store(p.key_img[tail] + at, smem_addr(sK), (uint32_t)kImageBytes);
-    bulk_store(p.val_img[tail] + at, smem_addr(sV), (uint32_t)kImageBytes);
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-  }
+  const int64_t at = (((tail ? (int64_t)b * p.Hn : 0) + hl) * nt + j) * kImageBytes;
+  if (!values) expand_tile<TT, true, PRECISE>(p, nlut, tail, h, b, tile0, n, p.key_img[tail] + at, p.val_img[tail] + at);
+  else expand_tile<TT, false, false>(p, nlut, tail, h, b, tile0, n, p.val_img[tail] + at, nullptr);
 }
 
 template <int TT>
@@ -169,14 +238,9 @@ cudaError_t expand_t(const BatchParams& p, bool precise, cudaStream_t s) {
   // the launch's key tiles and rows: none of a part that another kernel handles
   const int64_t tiles_p = p.S1 > 0 ? p.Hn * p.nt1 : 0, tiles_t = p.S2 > 0 ? p.B * p.Hn * p.nt2 : 0;
   const int64_t rows_h = p.S1 > 0 ? p.Hn * (p.Rp / 128) : 0, rows_s = p.S2 > 0 ? p.B * p.Hn * (p.RBp / 128) : 0;
-  const unsigned grid = (unsigned)(tiles_p + tiles_t + rows_h + rows_s);
-  const size_t smem = 1024 + 2 * (size_t)kImageBytes;
-  const void* k = precise ? reinterpret_cast<const void*>(qvg_batch_expand<TT, true>)
-                          : reinterpret_cast<const void*>(qvg_batch_expand<TT, false>);
-  const cudaError_t e = ensure_dynamic_smem(k, smem);
-  if (e != cudaSuccess) return e;
-  if (precise) qvg_batch_expand<TT, true><<<grid, kExThreads, smem, s>>>(p, tiles_p, tiles_t, rows_h);
-  else qvg_batch_expand<TT, false><<<grid, kExThreads, smem, s>>>(p, tiles_p, tiles_t, rows_h);
+  const unsigned grid = (unsigned)((precise ? 1 : 2) * (tiles_p + tiles_t) + rows_h + rows_s);
+  if (precise) qvg_batch_expand<TT, true><<<grid, kExThreads, 0, s>>>(p, tiles_p, tiles_t, rows_h);
+  else qvg_batch_expand<TT, false><<<grid, kExThreads, 0, s>>>(p, tiles_p, tiles_t, rows_h);
   return cudaGetLastError();
 }
 

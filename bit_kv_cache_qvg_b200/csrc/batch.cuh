@@ -51,6 +51,8 @@ struct BatchParams {
   uint8_t* val_img[2];            // the same of V (or of the keys' low halves)
   uint8_t* row_img[2];            // rows by head [Hn][2][Rp][128 B], and by sequence [B][Hn][2][RBp][128 B]
   uint8_t* row_lo[2];             // the rows' low halves
+  float* lse;                     // [Hn][Rp]: log2 of the rows' sums (weights)
+  int* limits;                    // [Hn][Rp]
   uint32_t* status;
 };
 
@@ -61,6 +63,8 @@ cudaError_t launch_rows_weights(const BatchParams& p, const float* received, flo
 cudaError_t launch_batch_merge(const BatchParams& p, cudaStream_t s);
 cudaError_t launch_batch_expand(const BatchParams& p, bool precise, cudaStream_t s);     // kernel_batch_expand.cu
 cudaError_t launch_batch_attend(const BatchParams& p, cudaStream_t s);                   // kernel_batch_attend.cu
+cudaError_t launch_batch_stats(const BatchParams& p, cudaStream_t s);                    // kernel_batch_weights.cu
+cudaError_t launch_batch_weights(const BatchParams& p, float* lse, int* limits, const float* received, float* out, cudaStream_t s);
 
 namespace {
 

@@ -43,18 +43,6 @@ struct __align__(8) AdShared {
   int abort_flag;
 };
 
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src),
-               "r"(bytes), "r"(smem_addr(bar))
-               : "memory");
-}
-__device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void bar_init(uint64_t* bar, uint32_t count) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count));
-}
-
 // B operand of O += P V: V's image holds a key's 64 channels of a half in 128
 // bytes, so B is N-major: 64 channels to the swizzled row, the other half
 // LBO = 16 KB on, 8 keys to the 1,024-byte group (SBO).  K-step kk takes keys
@@ -77,31 +65,6 @@ __device__ __forceinline__ void mma_values(uint32_t tmem_d, uint32_t tmem_a, uin
       "r"(tmem_a), "l"(b), "r"(kIdesc | (1u << 16)), "r"(accumulate)
       : "memory");
 }
-
-// 32 columns of the thread's lane, without the wait
-__device__ __forceinline__ void tld32_start(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
-        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
-        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
-        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr));
-}
-// the registers of a started load, not to be used before this
-__device__ __forceinline__ void hold32(uint32_t (&r)[32]) {
-  asm volatile(
-      ""
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-        "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-        "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-        "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
-}
-__device__ __forceinline__ void tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 // What a CTA has to do.
 struct AdPlace {
@@ -451,7 +414,11 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
     p.key_img[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.nt1 * kImageBytes));
     p.val_img[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.nt1 * kImageBytes));
     p.row_img[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.Rp * kD * 2));
-    if (!values) p.row_lo[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.Rp * kD * 2));
+    if (!values) {
+      p.row_lo[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.Rp * kD * 2));
+      p.lse = reinterpret_cast<float*>(take((size_t)plan.Hn * p.Rp * sizeof(float)));
+      p.limits = reinterpret_cast<int*>(take((size_t)plan.Hn * p.Rp * sizeof(int)));
+    }
   }
   if (plan.tc2) {
     p.key_img[1] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.B * p.nt2 * kImageBytes));
@@ -471,7 +438,7 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
 BatchPlan plan_batch(BatchParams& p, bool values) {
   BatchPlan plan{};
   const double sms = (double)device_sm_count();
-  plan.tc1 = values && p.R > kManyRows;
+  plan.tc1 = p.R > kManyRows;
   plan.tc2 = plan.tc1 && p.Nt > 0 && p.RB > kManyRows;
   plan.Hn = p.H;
   if (!plan.tc1) {
@@ -558,10 +525,18 @@ cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, 
   BatchParams p = params_of(a);
   const BatchPlan plan = plan_batch(p, false);
   place(p, plan, false, static_cast<char*>(ws));
+  cudaError_t e = cudaSuccess;
   const BatchParams few = share(p, plan, false);
-  const cudaError_t e = launch_rows_partial(few, false, s);
-  if (e != cudaSuccess) return e;
-  return launch_rows_weights(p, received, out, s);
+  if (few.S1 + few.S2 > 0 && (e = launch_rows_partial(few, false, s)) != cudaSuccess) return e;
+  if (!plan.tc1) return launch_rows_weights(p, received, out, s);
+  BatchParams q = share(p, plan, true);
+  for (q.h0 = 0; q.h0 < p.H; q.h0 += plan.Hn) {
+    q.Hn = std::min(plan.Hn, p.H - q.h0);
+    if ((e = launch_batch_expand(q, true, s)) != cudaSuccess) return e;
+    if ((e = launch_batch_stats(q, s)) != cudaSuccess) return e;
+    if ((e = launch_batch_weights(q, p.lse, p.limits, received, out, s)) != cudaSuccess) return e;
+  }
+  return e;
 }
 
 }  // namespace qvg

@@ -1,0 +1,377 @@
+// kernel_batch_weights.cu -- qvg_attention_weights for many rows, on tcgen05.
+//
+// The weight of key j is sum_r 2^(x_rj - lse_r), x_rj = sl q_r.k_j, lse_r the
+// base-2 logarithm of row r's sum over all its keys: a pass over the rows'
+// scores for lse, and a second one for the sums by key.  Both are one kernel:
+// two tiles of 128 stay in shared memory (rows in the first pass, keys in the
+// second) while the others stream by, and each of 256 threads reduces the
+// scores of its own row or key over the stream.  In the second pass the keys are the
+// M side of the product, so a key's sum stays in one thread and is taken
+// in one order, without atomics.
+//
+// A score must be good to fp32 (a sum of weights is an fp32 result), so each
+// operand is two bf16 halves and a score three products, high x high, low x
+// high and high x low: 24 tensor instructions a pair of tiles; the products are
+// the bound.
+// Stream tiles come as a high and a low half of 32 KB through a ring of three
+// slots; the scores are double-buffered in tensor memory, 128 columns for each
+// of two resident tiles.  Ten warps as in kernel_batch_attend.cu, all waits
+// bounded.
+#include "attention_tc.cuh"
+#include "batch.cuh"
+
+namespace qvg {
+namespace {
+
+constexpr int kWtThreads = 320;                   // 8 reducing warps, the issuer's, the loader's
+constexpr int kWtSlots = 3;                       // ring of half tiles
+
+struct __align__(16) WtShared {
+  float lse[2][kAtTile];          // of the streamed rows (second pass)
+  uint64_t full[kWtSlots], empty[kWtSlots];
+  uint64_t resident;
+  uint64_t s_done[2][2];          // scores of resident tile g in buffer i complete
+  uint64_t s_free[2][2];          // and read: 128 arrivals
+  uint64_t v_full[2], v_free[2];  // lse buffers: 128 arrivals of each resident tile free them
+  uint64_t drained;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// What a CTA has to do.  First pass (STATS): rows r0 .. of head h over tiles
+// j0 .. of the prefix's or a tail's keys.  Second: keys 256 tile .. over all
+// rows.
+struct WtPlace {
+  bool tail;
+  int hl, h, b, slot;
+  int n;                          // keys of the prefix or tail
+  int j0, steps;                  // stream tiles
+  int first, end;                 // resident rows (of the head) or keys
+  int groups;
+};
+template <bool STATS>
+__device__ __forceinline__ WtPlace wt_place(const BatchParams& p) {
+  WtPlace a;
+  if (STATS) {
+    const int64_t first_tail = (int64_t)p.S1 * p.tiles1 * p.Hn;
+    a.tail = blockIdx.x >= first_tail;
+    const int64_t e = a.tail ? blockIdx.x - first_tail : blockIdx.x;
+    const int S = a.tail ? p.S2 : p.S1;
+    const int64_t nb = a.tail ? p.tiles2 : p.tiles1;
+    const int range = (int)(e % S);
+    const int64_t block = e / S % nb, unit = e / S / nb;
+    a.hl = (int)(unit % p.Hn);
+    a.b = (int)(unit / p.Hn);
+    a.n = (int)(a.tail ? tail_length(p, a.b) : p.Nk);
+    a.slot = a.tail ? p.slot2 + range : range;
+    a.first = (int)((a.tail ? a.b * p.RB : 0) + block * 2 * kAtTile);
+    a.end = (int)(a.tail ? (a.b + 1) * p.RB : p.R);
+    const int64_t nt = (a.n + kAtTile - 1) / kAtTile;
+    a.j0 = (int)(nt * range / S);
+    a.steps = (int)(nt * (range + 1) / S) - a.j0;
+  } else {
+    const int64_t per = (p.nt1 + 1) / 2;
+    a.tail = false;
+    a.hl = (int)(blockIdx.x / per);
+    a.b = 0;
+    a.slot = 0;
+    a.n = (int)p.Nk;
+    a.first = (int)(blockIdx.x % per) * 2 * kAtTile;
+    a.end = a.n;
+    a.j0 = 0;
+    a.steps = (int)((p.R + kAtTile - 1) / kAtTile);
+  }
+  a.h = p.h0 + a.hl;
+  a.groups = a.end - a.first > kAtTile ? 2 : 1;
+  return a;
+}
+
+template <bool STATS>
+__global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchParams p, const float* lse, const int* limits,
+                                                                  const float* received, float* out) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* own = smem;                              // resident tile g: high half at 2g tiles, low half after it
+  uint8_t* ring = own + 4 * kAtOpBytes;
+  WtShared* sh = reinterpret_cast<WtShared*>(ring + kWtSlots * kAtOpBytes);
+  volatile int* abort_flag = &sh->abort_flag;
+  const WtPlace a = wt_place<STATS>(p);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kWtSlots; ++i) { bar_init(&sh->full[i], 1); bar_init(&sh->empty[i], 1); }
+    bar_init(&sh->resident, 1);
+    bar_init(&sh->drained, 1);
+    for (int i = 0; i < 2; ++i) {
+      for (int g = 0; g < 2; ++g) { bar_init(&sh->s_done[g][i], 1); bar_init(&sh->s_free[g][i], kAtTile); }
+      bar_init(&sh->v_full[i], 1);
+      bar_init(&sh->v_free[i], (uint32_t)(a.groups * kAtTile));
+    }
+    sh->abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&sh->tmem_base)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = sh->tmem_base;              // scores of resident tile g in buffer i at column 256 g + 128 i
+
+  if (warp == 9) {
+    // ---------------------------------------------------------------- loader
+    if (lane == 0 && a.steps > 0) {
+      // key tiles are whole images; row tiles are two halves of 64 channels, Rp or RBp rows apart
+      const int64_t unit = (a.tail ? (int64_t)a.b * p.Hn : 0) + a.hl;
+      const int64_t nt = a.tail ? p.nt2 : p.nt1, pad = a.tail ? p.RBp : p.Rp;
+      auto load_keys = [&](uint32_t dst, int64_t tile, bool low, uint64_t* bar) {
+        bulk_load(dst, (low ? p.val_img : p.key_img)[a.tail] + (unit * nt + tile) * kImageBytes, (uint32_t)kImageBytes, bar);
+      };
+      auto load_rows = [&](uint32_t dst, int64_t row, bool low, uint64_t* bar) {
+        const uint8_t* src = (low ? p.row_lo : p.row_img)[a.tail] + (unit * 2 * pad + row) * 128;
+        bulk_load(dst, src, kAtHalfBytes, bar);
+        bulk_load(dst + kAtHalfBytes, src + pad * 128, kAtHalfBytes, bar);
+      };
+      expect_bytes(&sh->resident, (uint32_t)(2 * a.groups * kAtOpBytes));
+      for (int g = 0; g < a.groups; ++g)
+        for (int low = 0; low < 2; ++low) {
+          const uint32_t dst = smem_addr(own) + (2 * g + low) * kAtOpBytes;
+          if (STATS) load_rows(dst, a.first - (a.tail ? a.b * p.RB : 0) + g * kAtTile, low != 0, &sh->resident);
+          else load_keys(dst, a.first / kAtTile + g, low != 0, &sh->resident);
+        }
+      int issued = 0, vectors = 0;
+      for (int i = 0; i < 2 * a.steps; ++i) {
+        const int slot = i % kWtSlots, turn = i / kWtSlots, j = i >> 1;
+        if (turn > 0 && !bar_wait_or_abort(&sh->empty[slot], (uint32_t)((turn - 1) & 1), abort_flag)) { *abort_flag = 1; break; }
+        expect_bytes(&sh->full[slot], (uint32_t)kAtOpBytes);
+        const uint32_t dst = smem_addr(ring) + slot * kAtOpBytes;
+        if (STATS) load_keys(dst, a.j0 + j, (i & 1) != 0, &sh->full[slot]);
+        else load_rows(dst, (int64_t)j * kAtTile, (i & 1) != 0, &sh->full[slot]);
+        ++issued;
+        if (!STATS && (i & 1) == 0) {
+          if (j > 1 && !bar_wait_or_abort(&sh->v_free[j & 1], (uint32_t)(((j >> 1) - 1) & 1), abort_flag)) { *abort_flag = 1; break; }
+          const int64_t at = (int64_t)a.hl * p.Rp + (int64_t)j * kAtTile;
+          expect_bytes(&sh->v_full[j & 1], kAtTile * 4);
+          bulk_load(smem_addr(sh->lse[j & 1]), lse + at, kAtTile * 4, &sh->v_full[j & 1]);
+          ++vectors;
+        }
+      }
+      // no copy may be in flight when the CTA leaves
+      bar_wait(&sh->resident, 0);
+      for (int i = issued > kWtSlots ? issued - kWtSlots : 0; i < issued; ++i)
+        bar_wait(&sh->full[i % kWtSlots], (uint32_t)((i / kWtSlots) & 1));
+      for (int j = vectors > 2 ? vectors - 2 : 0; j < vectors; ++j) bar_wait(&sh->v_full[j & 1], (uint32_t)((j >> 1) & 1));
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- issuer
+    if (lane == 0 && a.steps > 0) {
+      bool ok = bar_wait_or_abort(&sh->resident, 0, abort_flag);
+      // columns += resident half `low` of tile g times the half tile in `slot`
+      auto product = [&](int g, int low, int slot, int buf, bool add) {
+        const uint32_t a0 = smem_addr(own) + (2 * g + low) * kAtOpBytes, b0 = smem_addr(ring) + slot * kAtOpBytes;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma(tmem + 256 * g + 128 * buf, op_desc_k(a0, kk), op_desc_k(b0, kk), add || kk > 0 ? 1u : 0u);
+      };
+      for (int j = 0; ok && j < a.steps; ++j) {
+        const int buf = j & 1, hi = 2 * j, lo = 2 * j + 1;
+        ok = bar_wait_or_abort(&sh->full[hi % kWtSlots], (uint32_t)((hi / kWtSlots) & 1), abort_flag);
+        for (int g = 0; ok && g < a.groups; ++g) {
+          if (j > 1) ok = bar_wait_or_abort(&sh->s_free[g][buf], (uint32_t)(((j >> 1) - 1) & 1), abort_flag);
+          if (!ok) break;
+          fence_after();
+          product(g, 0, hi % kWtSlots, buf, false);
+          product(g, 1, hi % kWtSlots, buf, true);
+        }
+        if (!ok) break;
+        mma_commit(&sh->empty[hi % kWtSlots]);
+        ok = bar_wait_or_abort(&sh->full[lo % kWtSlots], (uint32_t)((lo / kWtSlots) & 1), abort_flag);
+        if (!ok) break;
+        fence_after();
+        for (int g = 0; g < a.groups; ++g) {
+          product(g, 0, lo % kWtSlots, buf, true);
+          mma_commit(&sh->s_done[g][buf]);
+        }
+        mma_commit(&sh->empty[lo % kWtSlots]);
+      }
+      if (!ok) *abort_flag = 1;
+      // every product has finished (bounded) before the tensor memory is freed
+      mma_commit(&sh->drained);
+      bar_wait(&sh->drained, 0);
+    }
+  } else if ((warp >> 2) < a.groups) {
+    // ---------------------------------------------------------------- a thread's row (STATS) or key over the stream
+    const int g = warp >> 2, mine = a.first + g * kAtTile + (threadIdx.x & 127);
+    const uint32_t tD = tmem + 256 * g + ((uint32_t)(32 * (warp & 3)) << 16);
+    const bool in = mine < a.end;
+    const float2 sl2 = make_float2(p.sl, p.sl);
+    // STATS: the row's limit and the least of the warp's live rows; otherwise
+    // the key's position and the largest of the warp's keys
+    int limit = kLimitNone, bound = 0;
+    if (STATS) {
+      limit = in ? row_limit(p, query_pos(p, mine)) : kLimitNone;
+      bound = __reduce_min_sync(0xffffffffu, limit != kLimitNone ? limit : kPosNever);
+    } else {
+      limit = mask_pos(p, false, a.h, 0, in ? mine : a.n - 1, a.n);
+      bound = __reduce_max_sync(0xffffffffu, limit);
+    }
+    const bool in_order = STATS && !a.tail && p.k_pos == nullptr;
+    float m_run = kNoMax, total = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < a.steps; ++j) {
+      const int buf = j & 1;
+      bool masked = false;
+      int kp[4];                                     // positions of the streamed keys, or limits of the streamed rows
+      if (STATS) {
+        const int k0 = (a.j0 + j) * kAtTile, valid = min(a.n - k0, kAtTile);
+        masked = valid < kAtTile || (p.causal && in_order && k0 + valid - 1 > bound);
+        if (masked || (p.causal && !in_order)) {
+          bool over = false;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            kp[c] = mask_pos(p, a.tail, a.h, a.b, k0 + 32 * c + lane, a.n);
+            over |= kp[c] > bound;
+          }
+          masked = __any_sync(0xffffffffu, over);
+        }
+      } else {
+        if (p.causal) {
+          bool under = false;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            kp[c] = __ldg(limits + (int64_t)a.hl * p.Rp + j * kAtTile + 32 * c + lane);
+            under |= kp[c] < bound;
+          }
+          masked = __any_sync(0xffffffffu, under);
+        }
+        ok = bar_wait_or_abort(&sh->v_full[buf], (uint32_t)((j >> 1) & 1), abort_flag);
+      }
+      ok = ok && bar_wait_or_abort(&sh->s_done[g][buf], (uint32_t)((j >> 1) & 1), abort_flag);
+      if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+      fence_after();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tld32_start(tD + 128 * buf + 32 * c, s[c]);
+      tld_wait();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) hold32(s[c]);
+      fence_before();
+      mbar_arrive(&sh->s_free[g][buf]);              // the scores are in registers
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      if (STATS) {
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (__shfl_sync(0xffffffffu, kp[c], e) > limit) s[c][e] = 0xFF800000u;       // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = __uint_as_float(s[c][0]);
+#pragma unroll
+          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+        }
+        const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl;
+        const float m_new = fmaxf(m_run, mt);
+        const float2 nm2 = make_float2(-m_new, -m_new);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sl2, nm2);
+            sum[e & 1] = __fadd2_rn(sum[e & 1], make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+          }
+        total = total * exp2_approx(m_run - m_new) + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
+        m_run = m_new;
+      } else {
+        const float4* rows = reinterpret_cast<const float4*>(sh->lse[buf]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 l = rows[8 * c + e];
+            float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e]), __uint_as_float(s[c][4 * e + 1])), sl2, make_float2(-l.x, -l.y));
+            float2 y = __ffma2_rn(make_float2(__uint_as_float(s[c][4 * e + 2]), __uint_as_float(s[c][4 * e + 3])), sl2, make_float2(-l.z, -l.w));
+            if (masked) {
+              if (limit > __shfl_sync(0xffffffffu, kp[c], 4 * e)) x.x = -INFINITY;
+              if (limit > __shfl_sync(0xffffffffu, kp[c], 4 * e + 1)) x.y = -INFINITY;
+              if (limit > __shfl_sync(0xffffffffu, kp[c], 4 * e + 2)) y.x = -INFINITY;
+              if (limit > __shfl_sync(0xffffffffu, kp[c], 4 * e + 3)) y.y = -INFINITY;
+            }
+            sum[0] = __fadd2_rn(sum[0], make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+            sum[1] = __fadd2_rn(sum[1], make_float2(exp2_approx(y.x), exp2_approx(y.y)));
+          }
+        total += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
+        mbar_arrive(&sh->v_free[buf]);
+      }
+    }
+    if (!ok) *abort_flag = 1;
+    if (ok && in) {
+      if (STATS) {
+        p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + mine] = make_float2(m_run, limit == kLimitNone ? 0.0f : total);
+      } else {
+        const int64_t at = (int64_t)a.h * p.Nk + mine;
+        out[at] = (received != nullptr ? received[at] : 0.0f) + total;
+      }
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, 1u);
+  if (warp == 0) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// The rows' lse from the partial results, and their limits, for the second
+// pass: lse = +inf (every weight 0) for a row that sees nothing and behind the
+// last row, whose limits then ask for no mask.
+__global__ void __launch_bounds__(256) qvg_batch_lse(const BatchParams p, float* lse, int* limits) {
+  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (e >= p.Hn * p.Rp) return;
+  const int hl = (int)(e / p.Rp);
+  const int64_t r = e - hl * p.Rp, row = (int64_t)(p.h0 + hl) * p.R + r, stride = (int64_t)p.H * p.R;
+  float x = INFINITY;
+  int limit = kLimitAll;
+  if (r < p.R) {
+    float M = kNoMax, L = 0.0f;
+    for (int s = 0; s < p.slots; ++s) M = fmaxf(M, __ldg(p.part_ml + s * stride + row).x);
+    for (int s = 0; s < p.slots; ++s) {
+      const float2 ml = __ldg(p.part_ml + s * stride + row);
+      L += ml.y * exp2_approx(ml.x - M);
+    }
+    if (L != 0.0f) {
+      x = M + log2f(L);
+      limit = row_limit(p, query_pos(p, r));
+    }
+  }
+  lse[e] = x;
+  limits[e] = limit;
+}
+
+size_t wt_smem_bytes() { return 1024 + (size_t)(4 + kWtSlots) * kAtOpBytes + sizeof(WtShared); }
+
+}  // namespace
+
+cudaError_t launch_batch_stats(const BatchParams& p, cudaStream_t s) {
+  const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(qvg_batch_weights<true>), wt_smem_bytes());
+  if (e != cudaSuccess) return e;
+  const unsigned grid = (unsigned)(p.S1 * p.tiles1 * p.Hn + p.S2 * p.tiles2 * p.Hn * p.B);
+  qvg_batch_weights<true><<<grid, kWtThreads, wt_smem_bytes(), s>>>(p, nullptr, nullptr, nullptr, nullptr);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_batch_weights(const BatchParams& p, float* lse, int* limits, const float* received, float* out, cudaStream_t s) {
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(qvg_batch_weights<false>), wt_smem_bytes());
+  if (e != cudaSuccess) return e;
+  qvg_batch_lse<<<(unsigned)((p.Hn * p.Rp + 255) / 256), 256, 0, s>>>(p, lse, limits);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  qvg_batch_weights<false><<<(unsigned)((p.nt1 + 1) / 2 * p.Hn), kWtThreads, wt_smem_bytes(), s>>>(p, lse, limits, received, out);
+  return cudaGetLastError();
+}
+
+}  // namespace qvg

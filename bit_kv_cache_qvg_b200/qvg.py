@@ -211,9 +211,9 @@ class Packed:
     dtype: int
 
     def struct(self) -> _Packed:
-        return _Packed(_ptr(self.codes), _ptr(self.scale), _ptr(self.zero) if self.zero.numel() else None,
-                       _ptr(self.assign) if self.assign.numel() else None,
-                       _ptr(self.centroids) if self.centroids.numel() else None)
+        # an empty tensor's address is 0
+        return _Packed(self.codes.data_ptr(), self.scale.data_ptr(), self.zero.data_ptr(), self.assign.data_ptr(),
+                       self.centroids.data_ptr())
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
@@ -363,44 +363,52 @@ class Tail:
     length: Optional[torch.Tensor] = None
 
 
-def _device_tensor(t: Optional[torch.Tensor], what: str, dtype, shape, device) -> Optional[torch.Tensor]:
-    """Check an argument's type, shape, layout and device (None passes)."""
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != device):
+def _device_tensor(t: Optional[torch.Tensor], what: str, dtype, shape, device) -> int:
+    """Check an argument's type, shape, layout and device; its address (None: 0)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise QvgError(1, f"{what} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
-    return t
+    return t.data_ptr()
 
 
-def _batch(p: Packed, Q: torch.Tensor, q_pos: torch.Tensor, k_pos, tail: Optional[Tail], causal: bool, values: bool) -> _Batch:
+def _batch(p: Packed, Q: torch.Tensor, q_pos: torch.Tensor, k_pos, tail: Optional[Tail], causal: bool, values: bool,
+           device) -> _Batch:
     if p.dtype != BF16:
         raise QvgError(2, "the cache must be a bf16 one")
     if Q.dim() != 4 or Q.shape[1] % p.H != 0 or Q.shape[3] != p.d:
         raise QvgError(1, "Q must be a [B][H * group][Nq][d] tensor")
-    dev, (B, Hq, Nq, d) = p.codes.device, Q.shape
-    _device_tensor(Q, "Q", torch.bfloat16, Q.shape, dev)
-    _device_tensor(q_pos, "q_pos", torch.int64, (B, Nq), dev)
-    _device_tensor(k_pos, "k_pos", torch.int64, (p.H, p.N), dev)
-    b = _Batch(B=B, group=Hq // p.H, Nq=Nq, Nt=0, Q=_ptr(Q), q_pos=_ptr(q_pos), k_pos=_ptr(k_pos), causal=1 if causal else 0)
-    if tail is not None and tail.k.dim() == 4 and tail.k.shape[2] > 0:
-        shape = (B, p.H, tail.k.shape[2], d)
-        if values and tail.v is None:
-            raise QvgError(1, "the tail has no values")
-        _device_tensor(tail.k, "the tail's k", torch.bfloat16, shape, dev)
-        _device_tensor(tail.v, "the tail's v", torch.bfloat16, shape, dev)
-        _device_tensor(tail.pos, "the tail's pos", torch.int64, (B, shape[2]), dev)
-        _device_tensor(tail.length, "the tail's length", torch.int32, (B,), dev)
-        b.Nt, b.tail_k, b.tail_v = shape[2], _ptr(tail.k), _ptr(tail.v)
-        b.tail_pos, b.tail_len = _ptr(tail.pos), _ptr(tail.length)
-    elif tail is not None and tail.k.dim() != 4:
+    B, Hq, Nq, d = Q.shape
+    H = p.H
+    at_q, at_pos = _device_tensor(Q, "Q", torch.bfloat16, Q.shape, device), _device_tensor(q_pos, "q_pos", torch.int64, (B, Nq), device)
+    at_k = _device_tensor(k_pos, "k_pos", torch.int64, (H, p.N), device)
+    if tail is None:
+        return _Batch(B, Hq // H, Nq, 0, at_q, at_pos, at_k, 0, 0, 0, 0, 1 if causal else 0)
+    k = tail.k
+    if k.dim() != 4:
         raise QvgError(1, "the tail's k must be a [B][H][Nt][d] tensor")
-    return b
+    Nt = k.shape[2]
+    shape = (B, H, Nt, d)
+    if values and tail.v is None:
+        raise QvgError(1, "the tail has no values")
+    return _Batch(B, Hq // H, Nq, Nt, at_q, at_pos, at_k, _device_tensor(k, "the tail's k", torch.bfloat16, shape, device),
+                  _device_tensor(tail.v, "the tail's v", torch.bfloat16, shape, device),
+                  _device_tensor(tail.pos, "the tail's pos", torch.int64, (B, Nt), device),
+                  _device_tensor(tail.length, "the tail's length", torch.int32, (B,), device), 1 if causal else 0)
 
 
 def _on_device(*tensors):
     """The device of the first tensor, a CUDA one, with the others on it."""
     dev = tensors[0].device
-    if dev.type != "cuda" or any(t is not None and t.device != dev for t in tensors):
+    if dev.type != "cuda" or any(t.device != dev for t in tensors):
         raise QvgError(1, "every tensor must be on the cache's CUDA device")
     return dev
+
+
+def _same_kind(kp: Packed, vp: Packed):
+    if vp.N != kp.N or vp.H != kp.H or vp.d != kp.d or vp.dtype != kp.dtype or \
+            (vp.cfg is not kp.cfg and bytes(vp.cfg) != bytes(kp.cfg)):
+        raise QvgError(1, "kp and vp must have the same sizes and configuration")
 
 
 def _lent(stream, *tensors):
@@ -413,19 +421,32 @@ def _lent(stream, *tensors):
                 t.record_stream(s)
 
 
+def _queue(dev, stream, call, *args) -> int:
+    """call(*args, stream) with `dev` as the current device; stream None: its current one."""
+    if torch.cuda.current_device() == dev.index:
+        return call(*args, torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream))
+    with torch.cuda.device(dev):
+        return call(*args, _stream(stream))
+
+
+def _workspace(workspace, size_call, p: Packed, b: _Batch, dev, stream) -> torch.Tensor:
+    if workspace is None:
+        if torch.cuda.current_device() == dev.index:
+            need = size_call(C.byref(p.cfg), p.N, p.H, C.byref(b))
+        else:
+            with torch.cuda.device(dev):
+                need = size_call(C.byref(p.cfg), p.N, p.H, C.byref(b))
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _lent(stream, workspace)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
+        raise QvgError(1, f"the workspace must be a contiguous uint8 tensor on {dev}")
+    return workspace
+
+
 def _tables(tables: torch.Tensor) -> torch.Tensor:
-    if tables.dtype != torch.uint8 or tables.dim() != 1 or not tables.is_contiguous():
+    if tables.dtype is not torch.uint8 or tables.dim() != 1 or not tables.is_contiguous():
         raise QvgError(1, "tables must be a tensor of rope_tables")
     return tables
-
-
-def _batch_workspace(workspace, need: int, device, stream):
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-        _lent(stream, workspace)
-    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous() or workspace.device != device:
-        raise QvgError(1, f"the workspace must be a contiguous uint8 tensor on {device}")
-    return workspace
 
 
 def attention_batch(kp: Packed, vp: Packed, Q: torch.Tensor, q_pos: torch.Tensor, tables: torch.Tensor,
@@ -437,22 +458,18 @@ def attention_batch(kp: Packed, vp: Packed, Q: torch.Tensor, q_pos: torch.Tensor
     row); k_pos [H][N] int64, the cached tokens' positions (None: 0 .. N-1);
     returns O, like Q, zeros in rows that see no key.  `workspace`: a uint8
     tensor of attention_batch_workspace_bytes (None: allocated here)."""
-    b = _batch(kp, Q, q_pos, k_pos, tail, causal, True)
-    if (vp.N, vp.H, vp.d, vp.dtype) != (kp.N, kp.H, kp.d, kp.dtype) or bytes(vp.cfg) != bytes(kp.cfg):
-        raise QvgError(1, "kp and vp must have the same sizes and configuration")
-    _device_tensor(O, "O", torch.bfloat16, Q.shape, Q.device)
-    dev = _on_device(kp.codes, vp.codes, _tables(tables))
-    with torch.cuda.device(dev):
-        need = 0 if workspace is not None else int(
-            lib().qvg_attention_batch_workspace_bytes(C.byref(kp.cfg), kp.N, kp.H, C.byref(b)))
-        ws = _batch_workspace(workspace, need, dev, stream)
-        if O is None:
-            O = torch.empty_like(Q)
-            _lent(stream, O)
-        ks, vs = kp.struct(), vp.struct()
-        _check(lib().qvg_attention_batch(C.byref(kp.cfg), C.byref(ks), C.byref(vs), kp.N, kp.H, kp.d, C.byref(b),
-                                         _ptr(tables), tables.numel(), _ptr(O), _ptr(ws), ws.numel(), _stream(stream)),
-               "qvg_attention_batch")
+    dev = kp.codes.device
+    b = _batch(kp, Q, q_pos, k_pos, tail, causal, True, dev)
+    _same_kind(kp, vp)
+    _device_tensor(O, "O", torch.bfloat16, Q.shape, dev)
+    _on_device(kp.codes, vp.codes, _tables(tables))
+    L = lib()
+    ws = _workspace(workspace, L.qvg_attention_batch_workspace_bytes, kp, b, dev, stream)
+    if O is None:
+        O = torch.empty_like(Q)
+        _lent(stream, O)
+    _check(_queue(dev, stream, L.qvg_attention_batch, C.byref(kp.cfg), C.byref(kp.struct()), C.byref(vp.struct()), kp.N, kp.H, kp.d,
+                  C.byref(b), tables.data_ptr(), tables.numel(), O.data_ptr(), ws.data_ptr(), ws.numel()), "qvg_attention_batch")
     return O
 
 
@@ -463,22 +480,20 @@ def attention_weights(kp: Packed, Q: torch.Tensor, q_pos: torch.Tensor, tables: 
     """qvg_attention_weights: received [H][N] fp32 (None: zeros) plus the softmax
     weight that each token of the prefix gets from the batch's rows (arguments
     as attention_batch).  `out` may be `received`, to add in place."""
-    b = _batch(kp, Q, q_pos, k_pos, tail, causal, False)
-    _device_tensor(out, "out", torch.float32, (kp.H, kp.N), Q.device)
-    _device_tensor(received, "received", torch.float32, (kp.H, kp.N), Q.device)
-    dev = _on_device(kp.codes, _tables(tables))
-    with torch.cuda.device(dev):
-        need = 0 if workspace is not None else int(
-            lib().qvg_attention_weights_workspace_bytes(C.byref(kp.cfg), kp.N, kp.H, C.byref(b)))
-        ws = _batch_workspace(workspace, need, dev, stream)
-        if out is None:
-            out = torch.empty((kp.H, kp.N), dtype=torch.float32, device=dev)
-            _lent(stream, out)
-        ks = kp.struct()
-        _check(lib().qvg_attention_weights(C.byref(kp.cfg), C.byref(ks), kp.N, kp.H, kp.d, C.byref(b), _ptr(tables),
-                                           tables.numel(), _ptr(received), _ptr(out), _ptr(ws), ws.numel(),
-                                           _stream(stream)),
-               "qvg_attention_weights")
+    dev = kp.codes.device
+    b = _batch(kp, Q, q_pos, k_pos, tail, causal, False, dev)
+    shape = (kp.H, kp.N)
+    _device_tensor(out, "out", torch.float32, shape, dev)
+    before = _device_tensor(received, "received", torch.float32, shape, dev)
+    _on_device(kp.codes, _tables(tables))
+    L = lib()
+    ws = _workspace(workspace, L.qvg_attention_weights_workspace_bytes, kp, b, dev, stream)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
+        _lent(stream, out)
+    _check(_queue(dev, stream, L.qvg_attention_weights, C.byref(kp.cfg), C.byref(kp.struct()), kp.N, kp.H, kp.d, C.byref(b),
+                  tables.data_ptr(), tables.numel(), before, out.data_ptr(), ws.data_ptr(), ws.numel()),
+           "qvg_attention_weights")
     return out
 
 
@@ -509,12 +524,11 @@ class Evicted:
 
 def _closed(p: Packed, keep: int) -> Packed:
     """Streams for `keep` tokens a head beside p's own centroid tables."""
-    ng, T = p.d // p.cfg.group_size, p.cfg.T
-    u8 = dict(dtype=torch.uint8, device=p.codes.device)
-    return Packed(codes=torch.empty((p.H, keep, p.d // 4), **u8), scale=torch.empty((p.H, keep, ng), **u8),
-                  zero=torch.empty((p.H, keep, ng) if p.cfg.scale_mode == ASYM else (0,), **u8),
-                  assign=torch.empty((T, p.H, keep), **u8), centroids=p.centroids,
-                  cfg=p.cfg, N=keep, H=p.H, d=p.d, dtype=p.dtype)
+    ng, H = p.d // p.cfg.group_size, p.H
+    new = p.codes.new_empty
+    return Packed(codes=new((H, keep, p.d // 4)), scale=new((H, keep, ng)),
+                  zero=new((H, keep, ng) if p.cfg.scale_mode == ASYM else (0,)), assign=new((p.cfg.T, H, keep)),
+                  centroids=p.centroids, cfg=p.cfg, N=keep, H=H, d=p.d, dtype=p.dtype)
 
 
 def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int = 0, recent: int = 0,
@@ -522,25 +536,22 @@ def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int =
     """qvg_evict: keep the first `first` and the last `recent` tokens of every
     head and, up to `keep` in all, those with the largest weights [H][N] fp32.
     The caches returned share the centroid tables of kp and vp."""
-    if (vp.N, vp.H, vp.d) != (kp.N, kp.H, kp.d) or bytes(vp.cfg) != bytes(kp.cfg):
-        raise QvgError(1, "kp and vp must have the same sizes and configuration")
+    _same_kind(kp, vp)
     if not 1 <= keep <= kp.N or first < 0 or recent < 0 or first + recent > keep:
         raise QvgError(1, "keep must be 1 .. N, first + recent at most keep")
-    _device_tensor(weights, "weights", torch.float32, (kp.H, kp.N), kp.codes.device)
-    _device_tensor(k_pos, "k_pos", torch.int64, (kp.H, kp.N), kp.codes.device)
-    dev = _on_device(kp.codes, vp.codes)
-    with torch.cuda.device(dev):
-        e = Evicted(k=_closed(kp, keep), v=_closed(vp, keep),
-                    kept=torch.empty((kp.H, keep), dtype=torch.int32, device=dev),
-                    pos=torch.empty((kp.H, keep), dtype=torch.int64, device=dev),
-                    weights=torch.empty((kp.H, keep), dtype=torch.float32, device=dev))
-        _lent(stream, e.kept, e.pos, e.weights,
-              *(t for p in (e.k, e.v) for t in (p.codes, p.scale, p.zero, p.assign)))
-        ks, vs, ko, vo = kp.struct(), vp.struct(), e.k.struct(), e.v.struct()
-        _check(lib().qvg_evict(C.byref(kp.cfg), C.byref(ks), C.byref(vs), kp.N, kp.H, kp.d, _ptr(weights), _ptr(k_pos), keep,
-                               first, recent, C.byref(ko), C.byref(vo), _ptr(e.kept), _ptr(e.pos), _ptr(e.weights),
-                               _stream(stream)),
-               "qvg_evict")
+    dev, shape = kp.codes.device, (kp.H, kp.N)
+    at_w = _device_tensor(weights, "weights", torch.float32, shape, dev)
+    at_pos = _device_tensor(k_pos, "k_pos", torch.int64, shape, dev)
+    _on_device(kp.codes, vp.codes)
+    e = Evicted(k=_closed(kp, keep), v=_closed(vp, keep),
+                kept=torch.empty((kp.H, keep), dtype=torch.int32, device=dev),
+                pos=torch.empty((kp.H, keep), dtype=torch.int64, device=dev),
+                weights=weights.new_empty((kp.H, keep)))
+    if stream is not None:
+        _lent(stream, e.kept, e.pos, e.weights, *(t for p in (e.k, e.v) for t in (p.codes, p.scale, p.zero, p.assign)))
+    _check(_queue(dev, stream, lib().qvg_evict, C.byref(kp.cfg), C.byref(kp.struct()), C.byref(vp.struct()), kp.N, kp.H, kp.d, at_w,
+                  at_pos, keep, first, recent, C.byref(e.k.struct()), C.byref(e.v.struct()), e.kept.data_ptr(),
+                  e.pos.data_ptr(), e.weights.data_ptr()), "qvg_evict")
     return e
 
 

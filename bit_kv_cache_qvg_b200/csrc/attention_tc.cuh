@@ -30,6 +30,8 @@ __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
+// The clock (and the abort flag) are looked at only after 63 tries: reading the
+// timer takes longer than most waits.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
   const uint32_t addr = smem_addr(bar);
   uint64_t t0 = 0;
@@ -43,7 +45,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
         : "r"(addr), "r"(parity)
         : "memory");
     if (done) return true;
-    if ((it & 63u) == 0u) {
+    if ((it & 63u) == 63u) {
       uint64_t now;
       asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
       if (t0 == 0) t0 = now;
@@ -68,7 +70,7 @@ __device__ __forceinline__ bool bar_wait_or_abort(uint64_t* bar, uint32_t parity
         : "r"(addr), "r"(parity)
         : "memory");
     if (done) return true;
-    if ((it & 63u) == 0u) {
+    if ((it & 63u) == 63u) {
       if (*abort_flag) return false;
       uint64_t now;
       asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
@@ -92,7 +94,7 @@ __device__ __forceinline__ bool bar_wait_cluster(uint64_t* bar, uint32_t parity,
         : "r"(addr), "r"(parity)
         : "memory");
     if (done) return true;
-    if ((it & 63u) == 0u) {
+    if ((it & 63u) == 63u) {
       if (*abort_flag) return false;
       uint64_t now;
       asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
@@ -117,6 +119,13 @@ __device__ __forceinline__ bool named_bar_or(int id, int count, bool pred) {
 }
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// one arrival for a converged warp, after what its lanes did: the lanes' own
+// arrivals on one barrier would go one after another (256 of them took longer
+// than the tile's products)
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 // arrive on a barrier of another CTA of the cluster (shared::cluster
 // address), releasing this thread's earlier writes at cluster scope
@@ -330,6 +339,33 @@ __device__ __forceinline__ void hold32(uint32_t (&r)[32]) {
         "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
 }
 __device__ __forceinline__ void tld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Products issued by a converged warp, in a branch that one elected lane takes.
+// The instruction wants its operands in uniform registers.  When the compiler
+// can tell that the warp's index, the tensor-memory address and the loop's
+// bounds are uniform (they come from a shuffle) and that one lane is in the
+// branch (elect.sync), a 128 x 128 x 16 product issues every 64 cycles, the tensor
+// core's rate; from `lane == 0` in a branch on threadIdx it took 85 to 140.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
+template <class T>
+__device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
+// D += A B with A in tensor memory, as mma_ta, for another instruction descriptor
+__device__ __forceinline__ void mma_ta_as(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// The steps of an operand tile's descriptor: K-step kk (16 columns) of a K-major one.
+__device__ __forceinline__ uint64_t desc_step(int kk) {
+  return (uint64_t)((kk >> 2) * (kAtHalfBytes >> 4) + (kk & 3) * 2);
+}
 
 // Reconstruction of channels c0 .. c0+7 of the NR tokens tok0 .. tok0+NR-1
 // (those below Nk) of cache `which` (0 = K, 1 = V) of head h: y = s*q + m

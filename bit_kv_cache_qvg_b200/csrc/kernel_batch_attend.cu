@@ -5,7 +5,7 @@
 //
 // One CTA = 256 rows of one K/V head (two row tiles of 128) x a range of key
 // tiles, of the prefix (the rows of every sequence and query head share it)
-// or of one sequence's tail.  Ten warps:
+// or of one sequence's tail.  Eighteen warps:
 //   * one thread streams K and V tiles (32 KB bulk copies) through a ring of
 //     five slots, K0 V0 K1 V1 ...;
 //   * one thread issues the products, S_g = Q_g K'^T and O_g += P_g V for the
@@ -13,10 +13,11 @@
 //     accumulators in tensor memory; P read from tensor memory).  P_g lies over
 //     S_g's columns: the products run in the order they are issued, so S_g of
 //     the next tile follows O_g of this one without a wait;
-//   * four warps per row tile run its softmax, a thread per row, the row's 128
-//     scores in registers: while one tile's softmax runs, the other's products
-//     do.  The reference maximum rises only when a row's maximum exceeds it by
-//     more than 8 (base 2), so O is rescaled rarely.
+//   * eight warps per row tile run its softmax, two threads to a row with 64 of
+//     its scores in registers each; they exchange their maxima through shared
+//     memory.  While one tile's softmax runs, the other's products do.  The
+//     reference maximum rises only when a row's maximum exceeds it by more than
+//     8 (base 2), so O is rescaled rarely.
 // Every wait is bounded and gives up when another role has; the kernel then
 // records QVG_ERR_DEVICE_TIMEOUT in the tables' status word.
 #include <algorithm>
@@ -28,7 +29,7 @@
 namespace qvg {
 namespace {
 
-constexpr int kAdThreads = 320;                   // 8 softmax warps, the issuer's, the loader's
+constexpr int kAdThreads = 576;                   // 16 softmax warps, the issuer's, the loader's
 constexpr int kAdRows = 256;                      // rows per CTA
 constexpr int kAdSlots = 5;                       // ring of operand tiles
 constexpr int kAdMaxRanges = 16;                  // of the prefix
@@ -37,34 +38,26 @@ struct __align__(8) AdShared {
   uint64_t full[kAdSlots], empty[kAdSlots];
   uint64_t q_full;
   uint64_t s_done[2];             // S_g complete (and every product issued before it)
-  uint64_t p_full[2];             // P_g written, O_g rescaled: 128 arrivals
+  uint64_t p_full[2];             // P_g written, O_g rescaled: an arrival of each of 8 warps
   uint64_t drained;               // after a failed wait: every product issued is complete
   uint32_t tmem_base;
   int abort_flag;
+  __nv_bfloat16 top[2][2][kAtTile];   // the maxima of a row's two halves
 };
 
 // B operand of O += P V: V's image holds a key's 64 channels of a half in 128
 // bytes, so B is N-major: 64 channels to the swizzled row, the other half
-// LBO = 16 KB on, 8 keys to the 1,024-byte group (SBO).  K-step kk takes keys
-// 16 kk .. 16 kk + 15.
-__device__ __forceinline__ uint64_t value_desc(uint32_t saddr, int kk) {
+// LBO = 16 KB on, 8 keys to the 1,024-byte group (SBO).
+__device__ __forceinline__ uint64_t value_desc(uint32_t saddr) {
   uint64_t d = 0;
-  d |= (uint64_t)(((saddr + (uint32_t)kk * 2048u) >> 4) & 0x3FFF);
+  d |= (uint64_t)((saddr >> 4) & 0x3FFF);
   d |= (uint64_t)(kAtHalfBytes >> 4) << 16;     // LBO
   d |= (uint64_t)(1024 >> 4) << 32;             // SBO
   d |= (uint64_t)1 << 46;                       // version
   d |= (uint64_t)2 << 61;                       // SWIZZLE_128B
   return d;
 }
-// D += A B with A (P, bf16) in tensor memory and B N-major
-__device__ __forceinline__ void mma_values(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(tmem_d),
-      "r"(tmem_a), "l"(b), "r"(kIdesc | (1u << 16)), "r"(accumulate)
-      : "memory");
-}
+constexpr uint32_t kIdescValues = kIdesc | (1u << 16);      // B N-major
 
 // What a CTA has to do.
 struct AdPlace {
@@ -106,13 +99,13 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
   AdShared* sh = reinterpret_cast<AdShared*>(ring + kAdSlots * kAtOpBytes);
   volatile int* abort_flag = &sh->abort_flag;
   const AdPlace a = ad_place(p);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int ntiles = a.ntiles;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+  const int ntiles = uniform(a.ntiles), groups = uniform(a.groups);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kAdSlots; ++i) { bar_init(&sh->full[i], 1); bar_init(&sh->empty[i], 1); }
     bar_init(&sh->q_full, 1);
-    for (int g = 0; g < 2; ++g) { bar_init(&sh->s_done[g], 1); bar_init(&sh->p_full[g], kAtTile); }
+    for (int g = 0; g < 2; ++g) { bar_init(&sh->s_done[g], 1); bar_init(&sh->p_full[g], 8); }
     bar_init(&sh->drained, 1);
     sh->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -124,10 +117,10 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = sh->tmem_base;
+  const uint32_t tmem = uniform(sh->tmem_base);
   const uint32_t tS = tmem, tO = tmem + 256;        // S of row tile g at column 128 g, O at 256 + 128 g
 
-  if (warp == 9) {
+  if (warp == 17) {
     // ---------------------------------------------------------------- loader
     if (lane == 0 && ntiles > 0) {
       const int64_t pad = a.tail ? p.RBp : p.Rp, first = a.tail ? a.r0 - a.b * p.RB : a.r0;
@@ -154,59 +147,80 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
       for (int i = issued > kAdSlots ? issued - kAdSlots : 0; i < issued; ++i)
         bar_wait(&sh->full[i % kAdSlots], (uint32_t)((i / kAdSlots) & 1));
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     // ---------------------------------------------------------------- issuer
-    if (lane == 0 && ntiles > 0) {
-      bool ok = bar_wait_or_abort(&sh->q_full, 0, abort_flag);
-      auto wait_full = [&](int i) {
-        return bar_wait_or_abort(&sh->full[i % kAdSlots], (uint32_t)((i / kAdSlots) & 1), abort_flag);
-      };
-      auto scores = [&](int g, int j) {
-        const uint32_t a0 = smem_addr(sQ + g * kAtOpBytes), b0 = smem_addr(ring) + (2 * j % kAdSlots) * kAtOpBytes;
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma(tS + 128 * g, op_desc_k(a0, kk), op_desc_k(b0, kk), kk > 0 ? 1u : 0u);
-      };
-      ok = ok && wait_full(0);
-      if (ok) {
+    // After a failed wait the loop runs on without waiting or issuing.
+    if (ntiles > 0) {
+      bool dead = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead) dead = !bar_wait_or_abort(bar, parity, abort_flag);
+        dead = __any_sync(0xffffffffu, dead);
         fence_after();
-        for (int g = 0; g < a.groups; ++g) { scores(g, 0); mma_commit(&sh->s_done[g]); }
+      };
+      const uint64_t rows0 = op_desc(smem_addr(sQ)), keys0 = op_desc(smem_addr(ring)), vals0 = value_desc(smem_addr(ring));
+      constexpr uint32_t kTile = kAtOpBytes >> 4;
+      auto scores = [&](int g, uint32_t slot) {
+        const uint64_t a0 = rows0 + g * kTile, b0 = keys0 + slot * kTile;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma(tS + 128 * g, a0 + desc_step(kk), b0 + desc_step(kk), kk > 0 ? 1u : 0u);
+      };
+      wait(&sh->q_full, 0);
+      wait(&sh->full[0], 0);
+      if (!dead && elect_one()) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+          if (g < groups) {
+            scores(g, 0);
+            mma_commit(&sh->s_done[g]);
+          }
         mma_commit(&sh->empty[0]);
       }
-      for (int j = 0; ok && j < ntiles; ++j) {
-        const int iv = 2 * j + 1, ik = 2 * j + 2;
+      __syncwarp();
+      uint32_t slot = 1, turn = 0;                   // V's place in the ring, and which pass over it; K's next tile follows
+#pragma unroll 1
+      for (int j = 0; j < ntiles; ++j) {
+        const uint32_t next = slot + 1 == kAdSlots ? 0 : slot + 1;
+        const uint32_t next_turn = turn ^ (next == 0 ? 1u : 0u);
         const bool more = j + 1 < ntiles;
-        ok = wait_full(iv);
-        for (int g = 0; ok && g < a.groups; ++g) {
-          ok = bar_wait_or_abort(&sh->p_full[g], (uint32_t)(j & 1), abort_flag);
-          if (!ok) break;
-          fence_after();
-          const uint32_t b0 = smem_addr(ring) + (iv % kAdSlots) * kAtOpBytes;
+        wait(&sh->full[slot], turn);
+        if (more) wait(&sh->full[next], next_turn);
+        const uint64_t b0 = vals0 + slot * kTile;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_values(tO + 128 * g, tS + 128 * g + (uint32_t)(8 * kk), value_desc(b0, kk), (j > 0 || kk > 0) ? 1u : 0u);
-          if (g == a.groups - 1) mma_commit(&sh->empty[iv % kAdSlots]);
-          if (more) {
-            if (g == 0) ok = wait_full(ik);
-            if (!ok) break;
-            fence_after();
-            scores(g, j + 1);
+        for (int g = 0; g < 2; ++g) {
+          if (g >= groups) continue;
+          wait(&sh->p_full[g], (uint32_t)(j & 1));
+          if (!dead && elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)           // K-step kk: 16 keys, 2 KB on
+              mma_ta_as(tO + 128 * g, tS + 128 * g + (uint32_t)(8 * kk), b0 + (uint64_t)(kk * 128), kIdescValues,
+                        (j > 0 || kk > 0) ? 1u : 0u);
+            if (more) scores(g, next);
+            mma_commit(&sh->s_done[g]);                // without more: O_g is complete
+            if (g == groups - 1) {
+              mma_commit(&sh->empty[slot]);
+              if (more) mma_commit(&sh->empty[next]);
+            }
           }
-          mma_commit(&sh->s_done[g]);                  // the last one: O_g is complete
-          if (more && g == a.groups - 1) mma_commit(&sh->empty[ik % kAdSlots]);
+          __syncwarp();
         }
+        slot = next + 1 == kAdSlots ? 0 : next + 1;
+        turn = next_turn ^ (slot == 0 ? 1u : 0u);
       }
-      if (!ok) {
+      if (dead) {
         *abort_flag = 1;
         // let the products that were issued finish (bounded) before the tensor memory is freed
-        mma_commit(&sh->drained);
+        if (elect_one()) mma_commit(&sh->drained);
+        __syncwarp();
         bar_wait(&sh->drained, 0);
       }
     }
-  } else if ((warp >> 2) < a.groups) {
+  } else if ((warp >> 3) < a.groups) {
     // ---------------------------------------------------------------- softmax of row tile g
-    const int g = warp >> 2, qi = threadIdx.x & 127;
+    // two threads of warps four apart take columns 0 .. 63 and 64 .. 127 of a row
+    const int g = warp >> 3, side = (warp >> 2) & 1, qi = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t tSt = tS + 128 * g + lane_base, tOt = tO + 128 * g + lane_base;
+    const uint32_t tSt = tS + 128 * g + 64 * side + lane_base, tPt = tS + 128 * g + 32 * side + lane_base;
+    const uint32_t tOt = tO + 128 * g + 64 * side + lane_base;
     const int row = a.r0 + g * kAtTile + qi;
     const int limit = row < a.r1 ? row_limit(p, query_pos(p, row)) : kLimitNone;
     // the least limit of the warp's live rows
@@ -216,31 +230,31 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
     bool ok = true;
     for (int j = 0; j < ntiles; ++j) {
       // Does any live row of the warp miss a key of this tile?  Where positions
-      // are in order the last one tells; otherwise the lanes look at four each.
+      // are in order the last one tells; otherwise the lanes look at two each.
       const int k0 = (a.j0 + j) * kAtTile, valid = min(a.n - k0, kAtTile);
       bool masked = valid < kAtTile || (p.causal && in_order && k0 + valid - 1 > least);
-      int kp[4];
+      int kp[2];
       if (masked || (p.causal && !in_order)) {
         bool over = false;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          kp[c] = mask_pos(p, a.tail, a.h, a.b, k0 + 32 * c + lane, a.n);
+        for (int c = 0; c < 2; ++c) {
+          kp[c] = mask_pos(p, a.tail, a.h, a.b, k0 + 64 * side + 32 * c + lane, a.n);
           over |= kp[c] > least;
         }
         masked = __any_sync(0xffffffffu, over);
       }
       ok = bar_wait_or_abort(&sh->s_done[g], (uint32_t)(j & 1), abort_flag);
-      if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+      ok = !__any_sync(0xffffffffu, !ok);
       fence_after();
-      uint32_t s[4][32];
+      uint32_t s[2][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tld32_start(tSt + 32 * c, s[c]);
+      for (int c = 0; c < 2; ++c) tld32_start(tSt + 32 * c, s[c]);
       tld_wait();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) hold32(s[c]);
+      for (int c = 0; c < 2; ++c) hold32(s[c]);
       if (masked) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (__shfl_sync(0xffffffffu, kp[c], e) > limit) s[c][e] = 0xFF800000u;       // -inf
@@ -248,17 +262,22 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
       float mx[4];
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        mx[c] = __uint_as_float(s[c][0]);
+        mx[c] = __uint_as_float(s[c >> 1][16 * (c & 1)]);
 #pragma unroll
-        for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+        for (int e = 1; e < 16; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c >> 1][16 * (c & 1) + e]));
       }
-      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl;
+      // any common reference near the maximum serves: bf16 is near enough
+      const __nv_bfloat16 mine = __float2bfloat16_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      sh->top[g][side][qi] = mine;
+      // all of S_g is in registers too: P_g may overwrite it
+      if (named_bar_or(1 + g, 256, !ok)) { ok = false; break; }
+      const float mt = fmaxf(__bfloat162float(mine), __bfloat162float(sh->top[g][side ^ 1][qi])) * p.sl;
       const float m_new = mt > m_run + 8.0f ? mt : m_run;
       const float alpha = exp2_approx(m_run - m_new);
       const float2 sl2 = make_float2(p.sl, p.sl), nm2 = make_float2(-m_new, -m_new);
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 2; ++c) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
@@ -267,13 +286,13 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
           // the sum of the rounded weights, the ones the product uses
           sum[e & 1] = __fadd2_rn(sum[e & 1], make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)));
         }
-        tst16(tSt + 16 * c, w);
+        tst16(tPt + 16 * c, w);
       }
       l_run = l_run * alpha + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
       m_run = m_new;
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {           // rescale O_g
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < 4; ++c) {
           uint32_t rg[16];
           tld16(tOt + 16 * c, rg);
 #pragma unroll
@@ -283,28 +302,32 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       fence_before();
-      mbar_arrive(&sh->p_full[g]);
+      warp_arrive(&sh->p_full[g], lane);
     }
-    if (ok && ntiles > 0) {
-      ok = bar_wait_or_abort(&sh->s_done[g], (uint32_t)(ntiles & 1), abort_flag);
-      ok = !__any_sync(0xffffffffu, !ok);
+    if (ok) {
+      if (ntiles > 0) ok = bar_wait_or_abort(&sh->s_done[g], (uint32_t)(ntiles & 1), abort_flag);
       fence_after();
+      // the two sums of a row joined, through the row tile, which no product reads any more
+      float* sums = reinterpret_cast<float*>(sQ + g * kAtOpBytes);
+      sums[128 * side + qi] = l_run;
+      ok = !named_bar_or(1 + g, 256, !ok);
+      l_run += sums[128 * (side ^ 1) + qi];
     }
     if (!ok) *abort_flag = 1;
     if (ok) {
       const bool whole = p.slots == 1;                 // nothing to join: O itself
       const bool dead = limit == kLimitNone || l_run == 0.0f;
       const int64_t out = ((int64_t)a.slot * p.H + a.h) * p.R + row;
-      if (row < a.r1 && !whole) p.part_ml[out] = make_float2(m_run, dead ? 0.0f : l_run);
+      if (row < a.r1 && side == 0 && !whole) p.part_ml[out] = make_float2(m_run, dead ? 0.0f : l_run);
       const float inv = dead ? 0.0f : 1.0f / l_run;
       if (ntiles > 0) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t rg[32];
           tld32(tOt + 32 * c, rg);
           if (row >= a.r1) continue;
           if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.O + query_row(p, a.h, row) * kD + 32 * c);
+            uint4* dst = reinterpret_cast<uint4*>(p.O + query_row(p, a.h, row) * kD + 64 * side + 32 * c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               uint32_t w[4];
@@ -316,7 +339,7 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
               dst[e] = make_uint4(w[0], w[1], w[2], w[3]);
             }
           } else {
-            float4* dst = reinterpret_cast<float4*>(p.part_O + out * kD + 32 * c);
+            float4* dst = reinterpret_cast<float4*>(p.part_O + out * kD + 64 * side + 32 * c);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               dst[e] = make_float4(__uint_as_float(rg[4 * e]), __uint_as_float(rg[4 * e + 1]),

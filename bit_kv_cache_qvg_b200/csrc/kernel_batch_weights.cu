@@ -4,9 +4,9 @@
 // base-2 logarithm of row r's sum over all its keys: a pass over the rows'
 // scores for lse, and a second one for the sums by key.  Both are one kernel:
 // two tiles of 128 stay in shared memory (rows in the first pass, keys in the
-// second) while the others stream by, and each of 256 threads reduces the
-// scores of its own row or key over the stream.  In the second pass the keys are the
-// M side of the product, so a key's sum stays in one thread and is taken
+// second) while the others stream by, and two threads reduce the scores of
+// each resident row or key over the stream, 64 columns of a tile each.  In the second pass the keys are the
+// M side of the product, so a key's sum stays in its threads and is taken
 // in one order, without atomics.
 //
 // A score must be good to fp32 (a sum of weights is an fp32 result), so each
@@ -15,7 +15,7 @@
 // the bound.
 // Stream tiles come as a high and a low half of 32 KB through a ring of three
 // slots; the scores are double-buffered in tensor memory, 128 columns for each
-// of two resident tiles.  Ten warps as in kernel_batch_attend.cu, all waits
+// of two resident tiles.  Eighteen warps as in kernel_batch_attend.cu, all waits
 // bounded.
 #include "attention_tc.cuh"
 #include "batch.cuh"
@@ -23,7 +23,7 @@
 namespace qvg {
 namespace {
 
-constexpr int kWtThreads = 320;                   // 8 reducing warps, the issuer's, the loader's
+constexpr int kWtThreads = 576;                   // 16 reducing warps, the issuer's, the loader's
 constexpr int kWtSlots = 3;                       // ring of half tiles
 
 struct __align__(16) WtShared {
@@ -31,8 +31,8 @@ struct __align__(16) WtShared {
   uint64_t full[kWtSlots], empty[kWtSlots];
   uint64_t resident;
   uint64_t s_done[2][2];          // scores of resident tile g in buffer i complete
-  uint64_t s_free[2][2];          // and read: 128 arrivals
-  uint64_t v_full[2], v_free[2];  // lse buffers: 128 arrivals of each resident tile free them
+  uint64_t s_free[2][2];          // and read: an arrival of each of 8 warps
+  uint64_t v_full[2], v_free[2];  // lse buffers: 8 warps' arrivals for each resident tile free them
   uint64_t drained;
   uint32_t tmem_base;
   int abort_flag;
@@ -96,16 +96,16 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
   WtShared* sh = reinterpret_cast<WtShared*>(ring + kWtSlots * kAtOpBytes);
   volatile int* abort_flag = &sh->abort_flag;
   const WtPlace a = wt_place<STATS>(p);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kWtSlots; ++i) { bar_init(&sh->full[i], 1); bar_init(&sh->empty[i], 1); }
     bar_init(&sh->resident, 1);
     bar_init(&sh->drained, 1);
     for (int i = 0; i < 2; ++i) {
-      for (int g = 0; g < 2; ++g) { bar_init(&sh->s_done[g][i], 1); bar_init(&sh->s_free[g][i], kAtTile); }
+      for (int g = 0; g < 2; ++g) { bar_init(&sh->s_done[g][i], 1); bar_init(&sh->s_free[g][i], 8); }
       bar_init(&sh->v_full[i], 1);
-      bar_init(&sh->v_free[i], (uint32_t)(a.groups * kAtTile));
+      bar_init(&sh->v_free[i], (uint32_t)(a.groups * 8));
     }
     sh->abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -117,9 +117,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = sh->tmem_base;              // scores of resident tile g in buffer i at column 256 g + 128 i
+  const uint32_t tmem = uniform(sh->tmem_base);              // scores of resident tile g in buffer i at column 256 g + 128 i
 
-  if (warp == 9) {
+  if (warp == 17) {
     // ---------------------------------------------------------------- loader
     if (lane == 0 && a.steps > 0) {
       // key tiles are whole images; row tiles are two halves of 64 channels, Rp or RBp rows apart
@@ -163,47 +163,72 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
         bar_wait(&sh->full[i % kWtSlots], (uint32_t)((i / kWtSlots) & 1));
       for (int j = vectors > 2 ? vectors - 2 : 0; j < vectors; ++j) bar_wait(&sh->v_full[j & 1], (uint32_t)((j >> 1) & 1));
     }
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     // ---------------------------------------------------------------- issuer
-    if (lane == 0 && a.steps > 0) {
-      bool ok = bar_wait_or_abort(&sh->resident, 0, abort_flag);
-      // columns += resident half `low` of tile g times the half tile in `slot`
-      auto product = [&](int g, int low, int slot, int buf, bool add) {
-        const uint32_t a0 = smem_addr(own) + (2 * g + low) * kAtOpBytes, b0 = smem_addr(ring) + slot * kAtOpBytes;
+    const int steps = uniform(a.steps), groups = uniform(a.groups);
+    // after a failed wait the loop runs on without waiting or issuing
+    if (steps > 0) {
+      bool dead = false;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        if (!dead) dead = !bar_wait_or_abort(bar, parity, abort_flag);
+        dead = __any_sync(0xffffffffu, dead);
+        fence_after();
+      };
+      const uint64_t own0 = op_desc(smem_addr(own)), ring0 = op_desc(smem_addr(ring));
+      constexpr uint32_t kTile = kAtOpBytes >> 4;
+      // columns (+)= resident half `low` of tile g times the half tile in `slot`
+      auto product = [&](int g, int low, uint32_t slot, uint32_t columns, bool add) {
+        const uint64_t a0 = own0 + (2 * g + low) * kTile, b0 = ring0 + slot * kTile;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma(tmem + 256 * g + 128 * buf, op_desc_k(a0, kk), op_desc_k(b0, kk), add || kk > 0 ? 1u : 0u);
+          mma(columns + 256 * g, a0 + desc_step(kk), b0 + desc_step(kk), add || kk > 0 ? 1u : 0u);
       };
-      for (int j = 0; ok && j < a.steps; ++j) {
-        const int buf = j & 1, hi = 2 * j, lo = 2 * j + 1;
-        ok = bar_wait_or_abort(&sh->full[hi % kWtSlots], (uint32_t)((hi / kWtSlots) & 1), abort_flag);
-        for (int g = 0; ok && g < a.groups; ++g) {
-          if (j > 1) ok = bar_wait_or_abort(&sh->s_free[g][buf], (uint32_t)(((j >> 1) - 1) & 1), abort_flag);
-          if (!ok) break;
-          fence_after();
-          product(g, 0, hi % kWtSlots, buf, false);
-          product(g, 1, hi % kWtSlots, buf, true);
+      wait(&sh->resident, 0);
+      uint32_t hi = 0, lo = 1, hi_turn = 0, lo_turn = 0;     // slots of the two halves, and which pass over the ring
+      auto onward = [](uint32_t& slot, uint32_t& turn) {
+        slot += 2;
+        if (slot >= kWtSlots) { slot -= kWtSlots; turn ^= 1u; }
+      };
+#pragma unroll 1
+      for (int j = 0; j < steps; ++j) {
+        const uint32_t buf = (uint32_t)j & 1u, columns = tmem + 128 * buf;
+        wait(&sh->full[hi], hi_turn);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (g >= groups) continue;
+          if (j > 1) wait(&sh->s_free[g][buf], (uint32_t)(((j >> 1) - 1) & 1));
+          if (!dead && elect_one()) {
+            product(g, 0, hi, columns, false);
+            product(g, 1, hi, columns, true);
+            if (g == groups - 1) mma_commit(&sh->empty[hi]);
+          }
+          __syncwarp();
         }
-        if (!ok) break;
-        mma_commit(&sh->empty[hi % kWtSlots]);
-        ok = bar_wait_or_abort(&sh->full[lo % kWtSlots], (uint32_t)((lo / kWtSlots) & 1), abort_flag);
-        if (!ok) break;
-        fence_after();
-        for (int g = 0; g < a.groups; ++g) {
-          product(g, 0, lo % kWtSlots, buf, true);
-          mma_commit(&sh->s_done[g][buf]);
+        wait(&sh->full[lo], lo_turn);
+        if (!dead && elect_one()) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (g >= groups) continue;
+            product(g, 0, lo, columns, true);
+            mma_commit(&sh->s_done[g][buf]);
+          }
+          mma_commit(&sh->empty[lo]);
         }
-        mma_commit(&sh->empty[lo % kWtSlots]);
+        __syncwarp();
+        onward(hi, hi_turn);
+        onward(lo, lo_turn);
       }
-      if (!ok) *abort_flag = 1;
+      if (dead) *abort_flag = 1;
       // every product has finished (bounded) before the tensor memory is freed
-      mma_commit(&sh->drained);
+      if (elect_one()) mma_commit(&sh->drained);
+      __syncwarp();
       bar_wait(&sh->drained, 0);
     }
-  } else if ((warp >> 2) < a.groups) {
+  } else if ((warp >> 3) < a.groups) {
     // ---------------------------------------------------------------- a thread's row (STATS) or key over the stream
-    const int g = warp >> 2, mine = a.first + g * kAtTile + (threadIdx.x & 127);
-    const uint32_t tD = tmem + 256 * g + ((uint32_t)(32 * (warp & 3)) << 16);
+    // two threads of warps four apart take columns 0 .. 63 and 64 .. 127
+    const int g = warp >> 3, side = (warp >> 2) & 1, mine = a.first + g * kAtTile + (threadIdx.x & 127);
+    const uint32_t tD = tmem + 256 * g + 64 * side + ((uint32_t)(32 * (warp & 3)) << 16);
     const bool in = mine < a.end;
     const float2 sl2 = make_float2(p.sl, p.sl);
     // STATS: the row's limit and the least of the warp's live rows; otherwise
@@ -222,15 +247,15 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
     for (int j = 0; j < a.steps; ++j) {
       const int buf = j & 1;
       bool masked = false;
-      int kp[4];                                     // positions of the streamed keys, or limits of the streamed rows
+      int kp[2];                                     // positions of the streamed keys, or limits of the streamed rows
       if (STATS) {
         const int k0 = (a.j0 + j) * kAtTile, valid = min(a.n - k0, kAtTile);
         masked = valid < kAtTile || (p.causal && in_order && k0 + valid - 1 > bound);
         if (masked || (p.causal && !in_order)) {
           bool over = false;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            kp[c] = mask_pos(p, a.tail, a.h, a.b, k0 + 32 * c + lane, a.n);
+          for (int c = 0; c < 2; ++c) {
+            kp[c] = mask_pos(p, a.tail, a.h, a.b, k0 + 64 * side + 32 * c + lane, a.n);
             over |= kp[c] > bound;
           }
           masked = __any_sync(0xffffffffu, over);
@@ -239,8 +264,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
         if (p.causal) {
           bool under = false;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            kp[c] = __ldg(limits + (int64_t)a.hl * p.Rp + j * kAtTile + 32 * c + lane);
+          for (int c = 0; c < 2; ++c) {
+            kp[c] = __ldg(limits + (int64_t)a.hl * p.Rp + j * kAtTile + 64 * side + 32 * c + lane);
             under |= kp[c] < bound;
           }
           masked = __any_sync(0xffffffffu, under);
@@ -250,19 +275,19 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
       ok = ok && bar_wait_or_abort(&sh->s_done[g][buf], (uint32_t)((j >> 1) & 1), abort_flag);
       if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
       fence_after();
-      uint32_t s[4][32];
+      uint32_t s[2][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tld32_start(tD + 128 * buf + 32 * c, s[c]);
+      for (int c = 0; c < 2; ++c) tld32_start(tD + 128 * buf + 32 * c, s[c]);
       tld_wait();
 #pragma unroll
-      for (int c = 0; c < 4; ++c) hold32(s[c]);
+      for (int c = 0; c < 2; ++c) hold32(s[c]);
       fence_before();
-      mbar_arrive(&sh->s_free[g][buf]);              // the scores are in registers
+      warp_arrive(&sh->s_free[g][buf], lane);         // the scores are in registers
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
       if (STATS) {
         if (masked) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
               if (__shfl_sync(0xffffffffu, kp[c], e) > limit) s[c][e] = 0xFF800000u;       // -inf
@@ -270,15 +295,15 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(s[c][0]);
+          mx[c] = __uint_as_float(s[c >> 1][16 * (c & 1)]);
 #pragma unroll
-          for (int e = 1; e < 32; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c][e]));
+          for (int e = 1; e < 16; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c >> 1][16 * (c & 1) + e]));
         }
         const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.sl;
         const float m_new = fmaxf(m_run, mt);
         const float2 nm2 = make_float2(-m_new, -m_new);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sl2, nm2);
@@ -287,9 +312,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
         total = total * exp2_approx(m_run - m_new) + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
         m_run = m_new;
       } else {
-        const float4* rows = reinterpret_cast<const float4*>(sh->lse[buf]);
+        const float4* rows = reinterpret_cast<const float4*>(sh->lse[buf] + 64 * side);
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 l = rows[8 * c + e];
@@ -305,11 +330,28 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
             sum[1] = __fadd2_rn(sum[1], make_float2(exp2_approx(y.x), exp2_approx(y.y)));
           }
         total += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
-        mbar_arrive(&sh->v_free[buf]);
+        warp_arrive(&sh->v_free[buf], lane);
       }
     }
     if (!ok) *abort_flag = 1;
-    if (ok && in) {
+    // the row's or key's two halves joined, through the resident tile, which no
+    // product reads any more
+    float2* half = reinterpret_cast<float2*>(own + 2 * g * kAtOpBytes) + (threadIdx.x & 127);
+    if (STATS) {
+      if (side == 1) *half = make_float2(m_run, total);
+      named_bar_or(1 + g, 256, false);
+      if (side == 0) {
+        const float2 other = *half;
+        const float M = fmaxf(m_run, other.x);
+        total = total * exp2_approx(m_run - M) + other.y * exp2_approx(other.x - M);
+        m_run = M;
+      }
+    } else {
+      if (side == 1) half->x = total;
+      named_bar_or(1 + g, 256, false);
+      if (side == 0) total += half->x;
+    }
+    if (ok && in && side == 0) {
       if (STATS) {
         p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + mine] = make_float2(m_run, limit == kLimitNone ? 0.0f : total);
       } else {

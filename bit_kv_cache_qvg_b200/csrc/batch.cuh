@@ -42,6 +42,9 @@ struct BatchParams {
   float* part_O;                  // [slots][H][R][d]: unnormalised O of each range
   float2* part_ml;                // [slots][H][R]: (row maximum, row sum) of each range, base 2
   __nv_bfloat16* O;               // where a single slot needs no merge
+  int row_tiles;                  // tiles of 16 rows to a CTA of the kernels for few rows
+  float* scores;                  // [Hn][R][Nkp]: the prefix's scores, base 2 (weights of few rows)
+  int64_t Nkp;                    // Nk padded to 64
   // Tensor-core operands of heads h0 .. h0 + Hn - 1, laid out as the kernels'
   // shared memory wants them (kernel_batch_expand.cu).
   int h0, Hn;

@@ -373,9 +373,8 @@ cudaError_t launch_batch_attend(const BatchParams& p, cudaStream_t s) {
 // ---------------------------------------------------------------- plans
 namespace {
 
-constexpr int kRowTile = 16;                      // rows and keys of a step of the kernels for few rows
-constexpr int kRowStep = 64;
-constexpr int64_t kManyRows = 48;                 // rows beyond which tcgen05 takes over
+constexpr int kRowStep = 64;                      // keys of a step of the kernels for few rows
+constexpr int64_t kManyRows = 64;                 // rows beyond which tcgen05 takes over
 constexpr size_t kImageBudget = size_t(1) << 30;  // operand tiles in the workspace at a time, about
 
 BatchParams params_of(const BatchArgs& a) {
@@ -407,6 +406,8 @@ BatchParams params_of(const BatchArgs& a) {
   p.nt2 = (p.Nt + kAtTile - 1) / kAtTile;
   p.Rp = (p.R + kAdRows - 1) / kAdRows * kAdRows;
   p.RBp = (p.RB + kAdRows - 1) / kAdRows * kAdRows;
+  p.Nkp = (p.Nk + kRowStep - 1) / kRowStep * kRowStep;
+  p.Hn = p.H;
   return p;
 }
 
@@ -415,7 +416,8 @@ BatchParams params_of(const BatchArgs& a) {
 // when a sequence has.
 struct BatchPlan {
   bool tc1, tc2;                  // prefix, tails
-  int S1, S2, Hn;
+  int S1, S2, Hn;                 // ranges; heads at a time
+  int row_tiles;
   size_t bytes;
 };
 
@@ -433,6 +435,7 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
   const size_t rows = (size_t)p.H * p.R;
   if (values) p.part_O = reinterpret_cast<float*>(take(p.slots > 1 || !plan.tc1 ? p.slots * rows * kD * sizeof(float) : 0));
   p.part_ml = reinterpret_cast<float2*>(take(p.slots * rows * sizeof(float2)));
+  if (!values && !plan.tc1) p.scores = reinterpret_cast<float*>(take((size_t)plan.Hn * p.R * p.Nkp * sizeof(float)));
   if (plan.tc1) {
     p.key_img[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.nt1 * kImageBytes));
     p.val_img[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.nt1 * kImageBytes));
@@ -464,13 +467,17 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
   plan.tc1 = p.R > kManyRows;
   plan.tc2 = plan.tc1 && p.Nt > 0 && p.RB > kManyRows;
   plan.Hn = p.H;
+  const int64_t few = plan.tc1 ? p.RB : p.R;       // rows of the CTAs of the kernels for few rows
+  plan.row_tiles = few <= 16 ? 1 : few <= 32 ? 2 : 4;
+  const int64_t tile = 16 * plan.row_tiles;
   if (!plan.tc1) {
-    const int64_t units = (p.R + kRowTile - 1) / kRowTile * p.H;
+    if (!values) plan.Hn = (int)std::max<int64_t>(1, std::min<int64_t>(p.H, (int64_t)(kImageBudget / ((size_t)p.R * p.Nkp * sizeof(float)))));
+    const int64_t units = (p.R + tile - 1) / tile * plan.Hn;
     const int64_t most1 = (p.Nk + kRowStep - 1) / kRowStep;
     plan.S1 = (int)std::max<int64_t>(1, std::min<int64_t>({((int64_t)(4 * sms) + units - 1) / units, most1, 64}));
   }
   if (p.Nt > 0 && !plan.tc2) {
-    const int64_t units = (p.RB + kRowTile - 1) / kRowTile * p.H * p.B;
+    const int64_t units = (p.RB + tile - 1) / tile * plan.Hn * p.B;
     const int64_t most2 = (p.Nt + kRowStep - 1) / kRowStep;
     plan.S2 = (int)std::max<int64_t>(1, std::min<int64_t>({((int64_t)(4 * sms) + units - 1) / units, most2, 8}));
   }
@@ -506,7 +513,8 @@ BatchParams share(const BatchParams& p, const BatchPlan& plan, bool tc) {
   BatchParams q = p;
   q.S1 = plan.tc1 == tc ? plan.S1 : 0;
   q.S2 = plan.tc2 == tc ? plan.S2 : 0;
-  const int64_t tile = tc ? kAdRows : kRowTile;
+  q.row_tiles = plan.row_tiles;
+  const int64_t tile = tc ? kAdRows : 16 * plan.row_tiles;
   q.tiles1 = (p.R + tile - 1) / tile;
   q.tiles2 = (p.RB + tile - 1) / tile;
   return q;
@@ -549,9 +557,16 @@ cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, 
   const BatchPlan plan = plan_batch(p, false);
   place(p, plan, false, static_cast<char*>(ws));
   cudaError_t e = cudaSuccess;
-  const BatchParams few = share(p, plan, false);
-  if (few.S1 + few.S2 > 0 && (e = launch_rows_partial(few, false, s)) != cudaSuccess) return e;
-  if (!plan.tc1) return launch_rows_weights(p, received, out, s);
+  BatchParams few = share(p, plan, false);
+  if (!plan.tc1) {
+    for (few.h0 = 0; few.h0 < p.H; few.h0 += plan.Hn) {
+      few.Hn = std::min(plan.Hn, p.H - few.h0);
+      if ((e = launch_rows_partial(few, false, s)) != cudaSuccess) return e;
+      if ((e = launch_rows_weights(few, received, out, s)) != cudaSuccess) return e;
+    }
+    return e;
+  }
+  if (few.S2 > 0 && (e = launch_rows_partial(few, false, s)) != cudaSuccess) return e;
   BatchParams q = share(p, plan, true);
   for (q.h0 = 0; q.h0 < p.H; q.h0 += plan.Hn) {
     q.Hn = std::min(plan.Hn, p.H - q.h0);

@@ -617,7 +617,7 @@ static qvg_status check_batch(const qvg_config* cfg, int64_t Nk, int32_t H, int3
     return QVG_ERR_INVALID_ARG;
   const int64_t most = int64_t(1) << 23;
   if (b->Nq >= most || b->Nt >= most || (int64_t)b->B * b->group >= most || (int64_t)b->B * b->group * b->Nq >= most ||
-      (int64_t)H * b->B >= most)
+      (int64_t)H * b->B >= most || (int64_t)b->B * b->group * b->Nq * H >= (int64_t(1) << 31))
     return QVG_ERR_UNSUPPORTED;
   return QVG_OK;
 }

@@ -386,7 +386,8 @@ typedef struct {
  * weights are rounded to bf16) and fp32 sums.
  * Errors: INVALID_ARG (also Nk < 1, Nq < 1, B < 1, group < 1, Nt < 0, or
  * tables that do not cover Nk - 1 when k_pos is NULL), UNSUPPORTED (d != 128,
- * B * group * Nq or Nt of 2^23 or more), WORKSPACE_TOO_SMALL, CUDA,
+ * B * group * Nq, H * B or Nt of 2^23 or more, B * group * Nq * H of 2^31 or
+ * more), WORKSPACE_TOO_SMALL, CUDA,
  * DEVICE_TIMEOUT (recorded in the tables' status word by earlier work). */
 QVG_API qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* k, const qvg_packed* v, int64_t Nk,
                                int32_t H, int32_t d, const qvg_batch* batch, const void* tables,

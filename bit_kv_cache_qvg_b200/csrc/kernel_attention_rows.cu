@@ -74,7 +74,7 @@ __device__ __forceinline__ Place place_of(const BatchParams& p, int rows_per_cta
 // from operands of two bf16 halves (three products: high x high, low x high,
 // high x low), so that they are good to fp32.
 template <int TT, int MT, bool VALUES>
-__global__ void __launch_bounds__(kRwThreads) qvg_attention_rows(const BatchParams p) {
+__global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchParams p) {
   constexpr int kRows = 16 * MT;
   constexpr int kWarpKeys = 16 * MT;              // of a step's 64
   constexpr int kTiles = kWarpKeys / 8;           // tiles of 8 keys of a warp
@@ -83,15 +83,16 @@ __global__ void __launch_bounds__(kRwThreads) qvg_attention_rows(const BatchPara
   __nv_bfloat16* sV = sK + kRwKeys * kRwPitch;                       // values, or the keys' low halves
   __nv_bfloat16* sQ = sV + kRwKeys * kRwPitch;                       // rows (high halves, then low)
   float2* nlut = reinterpret_cast<float2*>(sQ + (VALUES ? 1 : 2) * kRows * kRwPitch);
-  int* spos = reinterpret_cast<int*>(nlut + 16);
-  float2* sml = reinterpret_cast<float2*>(spos + kRwKeys);           // [4][16]: a warp's rows at the end
+  float2* sml = nlut + 16;                                           // [4][16]: a warp's rows at the end
+  int* spos = reinterpret_cast<int*>(sml + 64);                      // [2][64]: positions for the masks, by step
+  uint32_t* turn = reinterpret_cast<uint32_t*>(spos + 2 * kRwKeys);  // rows of the rotary table
+  using Block = Tokens<TT, kRwKeys>;
+  Block& tk = *reinterpret_cast<Block*>(turn + kRwKeys);
+  Block& tv = *reinterpret_cast<Block*>(reinterpret_cast<uint8_t*>(&tk) + Block::bytes(kD >> p.lgG));
   const Place a = place_of(p, kRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int mt = warp % MT, kg = warp / MT;       // the warp's rows and keys
-  if (threadIdx.x < 16) {
-    const float off = p.sym ? 2.0f : 0.0f;
-    nlut[threadIdx.x] = make_float2((float)(threadIdx.x & 3u) - off, (float)(threadIdx.x >> 2) - off);
-  }
+  fill_nlut(p, nlut);
   // the rows, rotated
   for (int e = threadIdx.x; e < kRows * 16; e += kRwThreads) {
     const int r = e >> 4, cb = e & 15;
@@ -119,44 +120,70 @@ __global__ void __launch_bounds__(kRwThreads) qvg_attention_rows(const BatchPara
   }
   // rebuilding: the lane's key of a pass and its chunks rc and rc + 8
   const int rc = threadIdx.x & 7, rkey = threadIdx.x >> 3;
-  const Rebuild<TT> keys(p, 0, a.h, rc);
-  const Rebuild<TT> vals(p, VALUES ? 1 : 0, a.h, rc);
+  const Rebuild<TT, kRwKeys> keys(p, 0, a.h, rc);
+  const Rebuild<TT, kRwKeys> vals(p, VALUES ? 1 : 0, a.h, rc);
   const __nv_bfloat16* tail_k = a.tail ? p.tail[0] + ((int64_t)a.b * p.H + a.h) * p.Nt * kD + 8 * rc : nullptr;
   const __nv_bfloat16* tail_v = a.tail && VALUES ? p.tail[1] + ((int64_t)a.b * p.H + a.h) * p.Nt * kD + 8 * rc : nullptr;
+  // The bytes of a step's tokens, a step ahead in registers: threads 0 .. 63 have
+  // a key each, 64 .. 127 a value, and every thread a half of both's codes.
+  const int own = threadIdx.x & (kRwKeys - 1), w = threadIdx.x >> 6;
+  TokenBytes<TT> held;
+  uint4 held_codes[2];
+  int64_t held_pos = 0;
+  auto fetch = [&](int k0) {
+    const int key = min(k0 + own, a.n - 1);
+    if (w == 0) held_pos = raw_key_pos(p, a.tail, a.h, a.b, key);
+    if (a.tail) return;
+    if (VALUES || w == 0) load_token<TT>(p, w, a.h, key, held);
+    const int64_t half = ((int64_t)a.h * p.Nk + min(k0 + (int)(threadIdx.x >> 1), a.n - 1)) * 2 + (threadIdx.x & 1);
+    held_codes[0] = __ldg(reinterpret_cast<const uint4*>(p.codes[0]) + half);
+    if (VALUES) held_codes[1] = __ldg(reinterpret_cast<const uint4*>(p.codes[1]) + half);
+  };
+  auto stash = [&](int k0, int parity) {
+    const int key = k0 + own;
+    if (w == 0) {
+      spos[parity * kRwKeys + own] = key < a.n ? clamp_pos(held_pos) : kPosNever;
+      turn[own] = (uint32_t)rope_row(p, held_pos);
+    }
+    if (a.tail) return;
+    if (VALUES || w == 0) store_token<TT, kRwKeys>(p, w, a.h, min(key, a.n - 1), held, w == 0 ? tk : tv, own);
+    tk.codes[threadIdx.x] = held_codes[0];
+    if (VALUES) tv.codes[threadIdx.x] = held_codes[1];
+  };
   // ldmatrix: a warp's rows of Q, 8 keys of K (four 8 x 8 tiles along the channels), 16 keys of V
   const uint32_t aQ = shared_addr(sQ + (16 * mt + (lane & 15)) * kRwPitch + 8 * (lane >> 4));
   const uint32_t aK = shared_addr(sK + (kWarpKeys * kg + (lane & 7)) * kRwPitch + 8 * (lane >> 3));
   const uint32_t aV = shared_addr(sV + (kWarpKeys * kg + (lane & 15)) * kRwPitch + 8 * (lane >> 4));
   constexpr uint32_t kLow = kRwKeys * kRwPitch * 2;          // from the keys' high halves to the low ones
-  __syncthreads();
+  if (a.k0 < a.k1) fetch(a.k0);
+  int parity = 0;
 #pragma unroll 1
-  for (int k0 = a.k0; k0 < a.k1; k0 += kRwKeys) {
-    if (threadIdx.x < kRwKeys) spos[threadIdx.x] = mask_pos(p, a.tail, a.h, a.b, k0 + threadIdx.x, a.n);
+  for (int k0 = a.k0; k0 < a.k1; k0 += kRwKeys, parity ^= 1) {
+    stash(k0, parity);
+    __syncthreads();                               // and the last step's products have read sK and sV
+    if (k0 + kRwKeys < a.k1) fetch(k0 + kRwKeys);
 #pragma unroll 2
     for (int pass = 0; pass < kRwKeys / 16; ++pass) {
-      const int at = pass * 16 + rkey, key = min(k0 + at, a.n - 1);
-      const bool in = k0 + at < a.n;
+      const int at = pass * 16 + rkey;
       uint4 x[2], y[2];
       if (!a.tail) {
-        keys(nlut, (uint32_t)key, x);
-        if (VALUES) vals(nlut, (uint32_t)key, y);
+        keys(nlut, tk, at, x);
+        if (VALUES) vals(nlut, tv, at, y);
       } else {
         // a tail's tokens are bf16 rows already; behind its length zeros
         x[0] = x[1] = y[0] = y[1] = make_uint4(0, 0, 0, 0);
-        if (in) {
-          const uint4* row = reinterpret_cast<const uint4*>(tail_k + (int64_t)key * kD);
+        if (k0 + at < a.n) {
+          const uint4* row = reinterpret_cast<const uint4*>(tail_k + (int64_t)(k0 + at) * kD);
           x[0] = __ldg(row);
           x[1] = __ldg(row + 8);
           if (VALUES) {
-            row = reinterpret_cast<const uint4*>(tail_v + (int64_t)key * kD);
+            row = reinterpret_cast<const uint4*>(tail_v + (int64_t)(k0 + at) * kD);
             y[0] = __ldg(row);
             y[1] = __ldg(row + 8);
           }
         }
       }
-      int64_t pos = key;
-      if (a.tail || p.k_pos != nullptr) pos = rope_row(p, raw_key_pos(p, a.tail, a.h, a.b, key));
-      const float4* cs = reinterpret_cast<const float4*>(p.rope + pos * (kD / 2) + 4 * rc);
+      const float4* cs = reinterpret_cast<const float4*>(p.rope + (int64_t)turn[at] * (kD / 2) + 4 * rc);
       uint4 hi[2], lo[2];
       turn_chunk<!VALUES>(cs, x[0], hi[0], lo[0]);
       turn_chunk<!VALUES>(cs + 16, x[1], hi[1], lo[1]);
@@ -200,7 +227,7 @@ __global__ void __launch_bounds__(kRwThreads) qvg_attention_rows(const BatchPara
     float top[2] = {kNoMax, kNoMax};
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const int2 pos = *reinterpret_cast<const int2*>(spos + kWarpKeys * kg + 8 * t + 2 * c);
+      const int2 pos = *reinterpret_cast<const int2*>(spos + parity * kRwKeys + kWarpKeys * kg + 8 * t + 2 * c);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         s[t][2 * i] = pos.x <= limit[i] ? s[t][2 * i] * p.sl : -INFINITY;
@@ -260,7 +287,6 @@ __global__ void __launch_bounds__(kRwThreads) qvg_attention_rows(const BatchPara
 #pragma unroll
         for (int i = 0; i < 2; ++i) l[i] += ex2(s[t][2 * i] - m[i]) + ex2(s[t][2 * i + 1] - m[i]);
     }
-    __syncthreads();
   }
   // the results of the warps with the same rows joined
 #pragma unroll
@@ -354,56 +380,64 @@ __global__ void __launch_bounds__(128) qvg_weights_rows(const BatchParams p, con
 }
 
 // The ranges of every row joined: O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
-// with M = max_s m_s, rounded to bf16; zeros for a row that sees nothing.  A
-// CTA of four warps per row, each with every fourth range, a lane per four channels.
+// with M = max_s m_s, rounded to bf16; zeros for a row that sees nothing.  W
+// warps to a row, each with every W-th range, a lane per four channels.
+template <int W>
 __global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p) {
   __shared__ float4 acc_s[4][32];
   __shared__ float2 ml_s[4];
-  const int64_t row = blockIdx.x, stride = p.R * p.H;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
+  const int64_t row = (int64_t)blockIdx.x * (4 / W) + warp / W, stride = p.R * p.H;
   float M = kNoMax, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (row < stride) {
 #pragma unroll 4
-  for (int s = warp; s < p.slots; s += 4) {
-    const float2 ml = __ldg(p.part_ml + s * stride + row);
-    if (ml.y == 0.0f) continue;                    // an empty range
-    const float4 x = __ldg(reinterpret_cast<const float4*>(p.part_O + (s * stride + row) * kD) + lane);
-    const float mn = fmaxf(M, ml.x), f = ex2(M - mn), w = ex2(ml.x - mn);
-    acc.x = acc.x * f + w * x.x; acc.y = acc.y * f + w * x.y; acc.z = acc.z * f + w * x.z; acc.w = acc.w * f + w * x.w;
-    L = L * f + w * ml.y;
-    M = mn;
+    for (int s = part; s < p.slots; s += W) {
+      const float2 ml = __ldg(p.part_ml + s * stride + row);
+      if (ml.y == 0.0f) continue;                  // an empty range
+      const float4 x = __ldg(reinterpret_cast<const float4*>(p.part_O + (s * stride + row) * kD) + lane);
+      const float mn = fmaxf(M, ml.x), f = ex2(M - mn), w = ex2(ml.x - mn);
+      acc.x = acc.x * f + w * x.x; acc.y = acc.y * f + w * x.y; acc.z = acc.z * f + w * x.z; acc.w = acc.w * f + w * x.w;
+      L = L * f + w * ml.y;
+      M = mn;
+    }
   }
-  acc_s[warp][lane] = acc;
-  if (lane == 0) ml_s[warp] = make_float2(M, L);
-  __syncthreads();
-  if (warp != 0) return;
-  float T = kNoMax;
+  if (W > 1) {
+    acc_s[warp][lane] = acc;
+    if (lane == 0) ml_s[warp] = make_float2(M, L);
+    __syncthreads();
+    if (part != 0) return;
+    float top = kNoMax;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) T = fmaxf(T, ml_s[w].x);
-  float sum = 0.0f;
-  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int w = 0; w < W; ++w) top = fmaxf(top, ml_s[warp + w].x);
+    L = 0.0f;
+    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = ex2(ml_s[w].x - T);
-    const float4 x = acc_s[w][lane];
-    acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
-    sum += f * ml_s[w].y;
+    for (int w = 0; w < W; ++w) {
+      const float f = ex2(ml_s[warp + w].x - top);
+      const float4 x = acc_s[warp + w][lane];
+      acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
+      L += f * ml_s[warp + w].y;
+    }
   }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  if (row >= stride) return;
+  const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   const int h = (int)(row / p.R);
   reinterpret_cast<uint2*>(p.O + query_row(p, h, row - (int64_t)h * p.R) * kD)[lane] =
       make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
 }
 
-size_t rows_smem(int mt, bool values) {
-  return (size_t)(2 * kRwKeys + (values ? 1 : 2) * 16 * mt) * kRwPitch * 2 + 16 * sizeof(float2) + kRwKeys * sizeof(int) +
-         64 * sizeof(float2);
+size_t rows_smem(int T, int G, int mt, bool values) {
+  const size_t tiles = (size_t)(2 * kRwKeys + (values ? 1 : 2) * 16 * mt) * kRwPitch * 2;
+  const size_t block = kRwKeys * (32 + sizeof(uint32_t) * (T >= 0 && T <= 4 ? (T > 0 ? T : 1) : kMaxT) + kD / G * sizeof(float2));
+  return tiles + (16 + 64) * sizeof(float2) + 3 * kRwKeys * sizeof(int) + (values ? 2 : 1) * block;
 }
 
 template <int TT, int MT, bool VALUES>
 cudaError_t launch_rows_mt(const BatchParams& p, cudaStream_t s) {
   const unsigned grid = (unsigned)(p.S1 * p.tiles1 * p.Hn + p.S2 * p.tiles2 * p.Hn * p.B);
-  const size_t smem = rows_smem(MT, VALUES);
+  const size_t smem = rows_smem(p.T, p.G, MT, VALUES);
+  static_assert(Tokens<TT, kRwKeys>::bytes(1) == kRwKeys * (32 + sizeof(uint32_t) * Tokens<TT, kRwKeys>::TR + sizeof(float2)), "block size");
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(qvg_attention_rows<TT, MT, VALUES>), smem);
   if (e != cudaSuccess) return e;
   qvg_attention_rows<TT, MT, VALUES><<<grid, kRwThreads, smem, s>>>(p);
@@ -431,6 +465,14 @@ cudaError_t launch_rows(const BatchParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// CTAs to an SM: four by their registers, fewer where the rows or small groups
+// need more shared memory.
+int rows_per_sm(const BatchParams& p, bool values) {
+  const size_t smem = rows_smem(p.T, p.G, p.row_tiles, values) + 1024;
+  const int n = (int)(size_t(228 * 1024) / smem);
+  return n < 4 ? n : 4;
+}
+
 cudaError_t launch_rows_partial(const BatchParams& p, bool values, cudaStream_t s) {
   return values ? launch_rows<true>(p, s) : launch_rows<false>(p, s);
 }
@@ -441,7 +483,9 @@ cudaError_t launch_rows_weights(const BatchParams& p, const float* received, flo
 }
 
 cudaError_t launch_batch_merge(const BatchParams& p, cudaStream_t s) {
-  qvg_batch_merge<<<(unsigned)(p.R * p.H), 128, 0, s>>>(p);
+  const int64_t rows = p.R * p.H;
+  if (p.slots > 8) qvg_batch_merge<4><<<(unsigned)rows, 128, 0, s>>>(p);
+  else qvg_batch_merge<1><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -375,6 +375,7 @@ namespace {
 
 constexpr int kRowStep = 64;                      // keys of a step of the kernels for few rows
 constexpr int64_t kManyRows = 64;                 // rows beyond which tcgen05 takes over
+constexpr int64_t kFewMaxRanges = 64;              // ranges of few rows
 constexpr size_t kImageBudget = size_t(1) << 30;  // operand tiles in the workspace at a time, about
 
 BatchParams params_of(const BatchArgs& a) {
@@ -455,8 +456,8 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
   return at;
 }
 
-// The cut of the keys.  For few rows: enough CTAs to fill the SMs four times
-// over, at least one step of keys to each.  For many: the plan with the least
+// The cut of the keys.  For few rows: ranges of equal length, as many as run at
+// the same time (a last wave of few CTAs would double the time).  For many: the plan with the least
 // estimated time, in key tiles of a CTA that holds an SM: a CTA of t tiles
 // takes t + 3 (its start and its end), the tails' CTAs fill the gaps of the
 // prefix's last wave first, and a range's partial results cost their way
@@ -469,17 +470,20 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
   plan.Hn = p.H;
   const int64_t few = plan.tc1 ? p.RB : p.R;       // rows of the CTAs of the kernels for few rows
   plan.row_tiles = few <= 16 ? 1 : few <= 32 ? 2 : 4;
-  const int64_t tile = 16 * plan.row_tiles;
-  if (!plan.tc1) {
-    if (!values) plan.Hn = (int)std::max<int64_t>(1, std::min<int64_t>(p.H, (int64_t)(kImageBudget / ((size_t)p.R * p.Nkp * sizeof(float)))));
-    const int64_t units = (p.R + tile - 1) / tile * plan.Hn;
-    const int64_t most1 = (p.Nk + kRowStep - 1) / kRowStep;
-    plan.S1 = (int)std::max<int64_t>(1, std::min<int64_t>({((int64_t)(4 * sms) + units - 1) / units, most1, 64}));
-  }
-  if (p.Nt > 0 && !plan.tc2) {
-    const int64_t units = (p.RB + tile - 1) / tile * plan.Hn * p.B;
-    const int64_t most2 = (p.Nt + kRowStep - 1) / kRowStep;
-    plan.S2 = (int)std::max<int64_t>(1, std::min<int64_t>({((int64_t)(4 * sms) + units - 1) / units, most2, 8}));
+  p.row_tiles = plan.row_tiles;
+  const int64_t tile = 16 * plan.row_tiles, room = (int64_t)sms * rows_per_sm(p, values);
+  const int64_t steps1 = plan.tc1 ? 0 : (p.Nk + kRowStep - 1) / kRowStep;
+  const int64_t steps2 = plan.tc2 ? 0 : (p.Nt + kRowStep - 1) / kRowStep;
+  if (!plan.tc1 && !values)
+    plan.Hn = (int)std::max<int64_t>(1, std::min<int64_t>(p.H, (int64_t)(kImageBudget / ((size_t)p.R * p.Nkp * sizeof(float)))));
+  if (steps1 + steps2 > 0) {
+    // ranges of equal length, as many as run at the same time
+    const int64_t units1 = (p.R + tile - 1) / tile * plan.Hn, units2 = (p.RB + tile - 1) / tile * plan.Hn * p.B;
+    const int64_t longest = std::max(steps1, steps2);
+    int64_t steps = std::max<int64_t>(1, (longest + kFewMaxRanges - 1) / kFewMaxRanges);
+    while (steps < longest && units1 * ((steps1 + steps - 1) / steps) + units2 * ((steps2 + steps - 1) / steps) > room) ++steps;
+    plan.S1 = (int)((steps1 + steps - 1) / steps);
+    plan.S2 = (int)((steps2 + steps - 1) / steps);
   }
   if (plan.tc1) {
     size_t per_head = (size_t)p.nt1 * 2 * kImageBytes;

@@ -11,10 +11,8 @@
 // the K-major operand of S = Q K'^T in this layout and V the N-major one of
 // O = P V.  The rows are rotated once, too.
 //
-// Eight lanes take a key, two 8-channel chunks each (c and c + 8), so a warp
-// reads 128 contiguous bytes of a centroid row and writes 128 of an image.  The
-// work is arithmetic on 16 values a lane; the bound is the 512 bytes written a
-// token.
+// The floor is the 512 bytes written a token; what bounds it is the
+// arithmetic of the rebuilding (rebuild.cuh).
 #include "attention_tc.cuh"
 #include "batch.cuh"
 #include "rebuild.cuh"
@@ -50,21 +48,41 @@ __device__ __forceinline__ void expand_rows(const BatchParams& p, bool by_sequen
 
 // One tile of K (rotated; PRECISE: and its low halves) or of V.
 template <int TT, bool KEYS, bool PRECISE>
-__device__ __forceinline__ void expand_tile(const BatchParams& p, const float2* nlut, bool tail, int h, int b, int tile0, int n,
+__device__ __forceinline__ void expand_tile(const BatchParams& p, uint8_t* smem, bool tail, int h, int b, int tile0, int n,
                                             uint8_t* img, uint8_t* img_lo) {
+  float2* nlut = reinterpret_cast<float2*>(smem);
+  uint32_t* turn = reinterpret_cast<uint32_t*>(nlut + 16);           // rows of the rotary table
+  Tokens<TT, kAtTile>& tokens = *reinterpret_cast<Tokens<TT, kAtTile>*>(turn + kAtTile);
+  constexpr int w = KEYS ? 0 : 1;
+  // a thread per token: its bytes, or its position
+  if (threadIdx.x < kAtTile) {
+    const int key = min(tile0 + (int)threadIdx.x, n - 1);            // past the end: the last token, finite and not used
+    if (!tail) {
+      TokenBytes<TT> x;
+      load_token<TT>(p, w, h, key, x);
+      store_token<TT, kAtTile>(p, w, h, key, x, tokens, threadIdx.x);
+    }
+  } else if (KEYS) {
+    const int at = threadIdx.x - kAtTile, key = min(tile0 + at, n - 1);
+    turn[at] = (uint32_t)rope_row(p, raw_key_pos(p, tail, h, b, key));
+  }
+  if (!tail) {
+    const int key = min(tile0 + (int)(threadIdx.x >> 1), n - 1);
+    tokens.codes[threadIdx.x] = __ldg(reinterpret_cast<const uint4*>(p.codes[w] + ((int64_t)h * p.Nk + key) * (kD / 4)) + (threadIdx.x & 1));
+    fill_nlut(p, nlut);
+  }
+  __syncthreads();
   const int c = threadIdx.x & 7, key0 = threadIdx.x >> 3;
   // a lane's place in the image does not depend on the pass: 32 keys on, the swizzle is the same
   const uint32_t place = (uint32_t)(key0 * 128 + ((c ^ (key0 & 7)) << 4));
-  auto put = [&](int pass, int key, uint4 (&x)[2]) {
+  auto put = [&](int pass, uint4 (&x)[2]) {
     uint8_t* dst = img + place + pass * (kExKeys * 128);
     if (!KEYS) {
       *reinterpret_cast<uint4*>(dst) = x[0];
       *reinterpret_cast<uint4*>(dst + kAtHalfBytes) = x[1];
       return;
     }
-    int64_t pos = key;
-    if (tail || p.k_pos != nullptr) pos = rope_row(p, raw_key_pos(p, tail, h, b, key));
-    const float4* cs = reinterpret_cast<const float4*>(p.rope + pos * (kD / 2) + 4 * c);
+    const float4* cs = reinterpret_cast<const float4*>(p.rope + (int64_t)turn[pass * kExKeys + key0] * (kD / 2) + 4 * c);
     uint4 hi[2], lo[2];
     turn_chunk<PRECISE>(cs, x[0], hi[0], lo[0]);
     turn_chunk<PRECISE>(cs + 16, x[1], hi[1], lo[1]);
@@ -77,17 +95,16 @@ __device__ __forceinline__ void expand_tile(const BatchParams& p, const float2* 
     }
   };
   if (!tail) {
-    const Rebuild<TT> rebuild(p, KEYS ? 0 : 1, h, c);
+    const Rebuild<TT, kAtTile> rebuild(p, w, h, c);
 #pragma unroll 2
     for (int pass = 0; pass < kExPasses; ++pass) {
-      const int key = min(tile0 + pass * kExKeys + key0, n - 1);     // past the end: the last token, finite and not used
       uint4 x[2];
-      rebuild(nlut, (uint32_t)key, x);
-      put(pass, key, x);
+      rebuild(nlut, tokens, pass * kExKeys + key0, x);
+      put(pass, x);
     }
   } else {
     // a tail's tokens are bf16 rows already; behind its length zeros
-    const __nv_bfloat16* rows = p.tail[KEYS ? 0 : 1] + ((int64_t)b * p.H + h) * p.Nt * kD + 8 * c;
+    const __nv_bfloat16* rows = p.tail[w] + ((int64_t)b * p.H + h) * p.Nt * kD + 8 * c;
 #pragma unroll 2
     for (int pass = 0; pass < kExPasses; ++pass) {
       const int key = tile0 + pass * kExKeys + key0;
@@ -97,7 +114,7 @@ __device__ __forceinline__ void expand_tile(const BatchParams& p, const float2* 
         x[0] = __ldg(row);
         x[1] = __ldg(row + 8);
       }
-      put(pass, min(key, n - 1), x);
+      put(pass, x);
     }
   }
 }
@@ -108,7 +125,7 @@ __device__ __forceinline__ void expand_tile(const BatchParams& p, const float2* 
 template <int TT, bool PRECISE>
 __global__ void __launch_bounds__(kExThreads) qvg_batch_expand(const BatchParams p, const int64_t tiles_p, const int64_t tiles_t,
                                                               const int64_t row_tiles) {
-  __shared__ float2 nlut[16];
+  extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kKinds = PRECISE ? 1 : 2;
   int64_t id = blockIdx.x;
   if (id >= kKinds * (tiles_p + tiles_t)) {
@@ -120,8 +137,9 @@ __global__ void __launch_bounds__(kExThreads) qvg_batch_expand(const BatchParams
     expand_rows<PRECISE>(p, by_sequence, (int)(unit % p.Hn), (int)(unit / p.Hn), id % per);
     return;
   }
-  const bool values = !PRECISE && (id & 1) != 0;
-  if (!PRECISE) id >>= 1;
+  // all K tiles first, then all V tiles: neighbouring CTAs read the same tables
+  const bool values = id >= tiles_p + tiles_t;
+  if (values) id -= tiles_p + tiles_t;
   const bool tail = id >= tiles_p;
   if (tail) id -= tiles_p;
   const int64_t nt = tail ? p.nt2 : p.nt1, unit = id / nt;
@@ -129,14 +147,9 @@ __global__ void __launch_bounds__(kExThreads) qvg_batch_expand(const BatchParams
   const int n = (int)(tail ? tail_length(p, b) : p.Nk);
   const int tile0 = j * kAtTile;
   if (tile0 >= n) return;                          // a tail's tile that nobody reads
-  if (threadIdx.x < 16) {
-    const float off = p.sym ? 2.0f : 0.0f;
-    nlut[threadIdx.x] = make_float2((float)(threadIdx.x & 3u) - off, (float)(threadIdx.x >> 2) - off);
-  }
-  __syncthreads();
   const int64_t at = (((tail ? (int64_t)b * p.Hn : 0) + hl) * nt + j) * kImageBytes;
-  if (!values) expand_tile<TT, true, PRECISE>(p, nlut, tail, h, b, tile0, n, p.key_img[tail] + at, p.val_img[tail] + at);
-  else expand_tile<TT, false, false>(p, nlut, tail, h, b, tile0, n, p.val_img[tail] + at, nullptr);
+  if (!values) expand_tile<TT, true, PRECISE>(p, smem, tail, h, b, tile0, n, p.key_img[tail] + at, p.val_img[tail] + at);
+  else expand_tile<TT, false, false>(p, smem, tail, h, b, tile0, n, p.val_img[tail] + at, nullptr);
 }
 
 template <int TT>
@@ -145,8 +158,9 @@ cudaError_t expand_t(const BatchParams& p, bool precise, cudaStream_t s) {
   const int64_t tiles_p = p.S1 > 0 ? p.Hn * p.nt1 : 0, tiles_t = p.S2 > 0 ? p.B * p.Hn * p.nt2 : 0;
   const int64_t rows_h = p.S1 > 0 ? p.Hn * (p.Rp / 128) : 0, rows_s = p.S2 > 0 ? p.B * p.Hn * (p.RBp / 128) : 0;
   const unsigned grid = (unsigned)((precise ? 1 : 2) * (tiles_p + tiles_t) + rows_h + rows_s);
-  if (precise) qvg_batch_expand<TT, true><<<grid, kExThreads, 0, s>>>(p, tiles_p, tiles_t, rows_h);
-  else qvg_batch_expand<TT, false><<<grid, kExThreads, 0, s>>>(p, tiles_p, tiles_t, rows_h);
+  const size_t smem = 16 * sizeof(float2) + kAtTile * sizeof(uint32_t) + Tokens<TT, kAtTile>::bytes(kD / p.G);
+  if (precise) qvg_batch_expand<TT, true><<<grid, kExThreads, smem, s>>>(p, tiles_p, tiles_t, rows_h);
+  else qvg_batch_expand<TT, false><<<grid, kExThreads, smem, s>>>(p, tiles_p, tiles_t, rows_h);
   return cudaGetLastError();
 }
 

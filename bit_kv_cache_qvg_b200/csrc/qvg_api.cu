@@ -674,7 +674,7 @@ qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* k, const
   qvg_status st = check_batch(cfg, Nk, H, d, batch);
   if (st != QVG_OK) return st;
   int64_t max_pos = 0;
-  if ((st = check_packed(cfg, k, 2, true)) != QVG_OK || (st = check_packed(cfg, v, 2, true)) != QVG_OK) return st;
+  if ((st = check_packed(cfg, k, 16, true)) != QVG_OK || (st = check_packed(cfg, v, 16, true)) != QVG_OK) return st;
   if ((st = check_batch_pointers(batch, Nk, true, tables, tables_bytes, workspace, &max_pos)) != QVG_OK) return st;
   if (O == nullptr || !aligned(O, 16)) return QVG_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
@@ -695,7 +695,7 @@ qvg_status qvg_attention_weights(const qvg_config* cfg, const qvg_packed* k, int
   qvg_status st = check_batch(cfg, Nk, H, d, batch);
   if (st != QVG_OK) return st;
   int64_t max_pos = 0;
-  if ((st = check_packed(cfg, k, 2, true)) != QVG_OK) return st;
+  if ((st = check_packed(cfg, k, 16, true)) != QVG_OK) return st;
   if ((st = check_batch_pointers(batch, Nk, false, tables, tables_bytes, workspace, &max_pos)) != QVG_OK) return st;
   if (out == nullptr || !aligned(out, 4) || !aligned(received, 4)) return QVG_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);

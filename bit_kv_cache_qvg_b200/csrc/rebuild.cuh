@@ -1,5 +1,14 @@
 // rebuild.cuh -- cached tokens rebuilt and rotated in registers, eight lanes to
 // a token, for the kernels of qvg_attention_batch and qvg_attention_weights.
+//
+// What belongs to a token as a whole (its codes, scales, centroid indices, its
+// row of the rotary table) is brought into shared memory by one thread each,
+// in the form in which the lanes use it; the eight lanes then take two 8-channel
+// chunks each (c and c + 8), so that a warp reads 128 contiguous bytes of a
+// centroid row and writes 128 of its result.  The arithmetic is that of
+// qvg_dequant_fused, about 75 instructions for 16 channels with one stage and
+// 105 with two; loading and decoding the token's bytes in every lane took a
+// third more.
 #pragma once
 
 #include "batch.cuh"
@@ -25,61 +34,119 @@ __device__ __forceinline__ void turn_chunk(const float4* cs, uint4 x, uint4& hi,
   turn_pair<PRECISE>(x.w, t1.z, t1.w, hi.w, lo.w);
 }
 
-// The reconstructed chunks c and c + 8 of a prefix token as packed bf16 pairs
-// (the arithmetic of qvg_dequant_fused).  The pointers are the head's; offsets
-// within a head fit in 32 bits.
-template <int TT>
-struct Rebuild {
-  const uint8_t *codes, *scale, *zero, *assign;
-  const __nv_bfloat16* tab;
-  int64_t assign_stage, tab_stage;
-  uint32_t top;                   // K - 1
-  int lgng, g0, g1, sym, T;       // log2(d/G), the chunks' groups
+// nibble -> two codes (q, or u - 2 in the symmetric mode)
+__device__ __forceinline__ void fill_nlut(const BatchParams& p, float2* nlut) {
+  if (threadIdx.x < 16) {
+    const float off = p.sym ? 2.0f : 0.0f;
+    nlut[threadIdx.x] = make_float2((float)(threadIdx.x & 3u) - off, (float)(threadIdx.x >> 2) - off);
+  }
+}
 
-  __device__ __forceinline__ Rebuild(const BatchParams& p, int w, int h, int c) {
-    lgng = 7 - p.lgG;
-    const int64_t row = (int64_t)h * p.Nk;
-    codes = p.codes[w] + row * (kD / 4) + 2 * c;
-    scale = p.scale[w] + (row << lgng);
-    zero = p.zero[w] + (p.sym ? 0 : (row << lgng));
-    assign = p.assign[w] + row;
-    tab = p.tab[w] + (int64_t)h * p.K * kD + 8 * c;
-    assign_stage = (int64_t)p.H * p.Nk;
-    tab_stage = (int64_t)p.H * p.K * kD;
-    top = (uint32_t)p.K - 1;
+// The bytes of NK tokens of one cache, in shared memory.  `sm` has room for
+// NK * d/G pairs (scale, zero point).
+template <int TT, int NK>
+struct Tokens {
+  static constexpr int TR = TT >= 0 ? (TT > 0 ? TT : 1) : kMaxT;
+  uint4 codes[NK * 2];
+  uint32_t row[TR][NK];           // byte offsets of the centroid rows in a head's stage table
+  static __host__ __device__ constexpr size_t bytes(int ng) { return sizeof(Tokens) + (size_t)NK * ng * sizeof(float2); }
+  __device__ __forceinline__ float2* sm() { return reinterpret_cast<float2*>(this + 1); }
+  __device__ __forceinline__ const float2* sm() const { return reinterpret_cast<const float2*>(this + 1); }
+};
+
+// What one thread holds of a token between loading and storing it (so that the
+// next block's bytes can be on their way while this one's are used).
+template <int TT>
+struct TokenBytes {
+  static constexpr int TR = TT > 0 ? TT : 1;
+  uint4 scale, zero;
+  uint32_t k[TR];
+};
+__device__ __forceinline__ uint4 load_bytes(const uint8_t* base, int64_t tok, int ng) {
+  uint4 r = make_uint4(0, 0, 0, 0);
+  switch (ng) {
+    case 1: r.x = __ldg(base + tok); break;
+    case 2: r.x = __ldg(reinterpret_cast<const uint16_t*>(base) + tok); break;
+    case 4: r.x = __ldg(reinterpret_cast<const uint32_t*>(base) + tok); break;
+    case 8: { const uint2 v = __ldg(reinterpret_cast<const uint2*>(base) + tok); r.x = v.x; r.y = v.y; break; }
+    default: r = __ldg(reinterpret_cast<const uint4*>(base) + tok);
+  }
+  return r;
+}
+template <int TT>
+__device__ __forceinline__ void load_token(const BatchParams& p, int w, int h, int tok, TokenBytes<TT>& x) {
+  const int64_t at = (int64_t)h * p.Nk + tok;
+  const int ng = kD >> p.lgG;
+  x.scale = load_bytes(p.scale[w], at, ng);
+  if (!p.sym) x.zero = load_bytes(p.zero[w], at, ng);
+  if (TT > 0) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      x.k[t] = min((uint32_t)__ldg(p.assign[w] + ((int64_t)t * p.H + h) * p.Nk + tok), (uint32_t)p.K - 1);
+  }
+}
+template <int TT, int NK>
+__device__ __forceinline__ void store_token(const BatchParams& p, int w, int h, int tok, const TokenBytes<TT>& x, Tokens<TT, NK>& to, int at) {
+  const int ng = kD >> p.lgG;
+  const uint32_t s[4] = {x.scale.x, x.scale.y, x.scale.z, x.scale.w}, z[4] = {x.zero.x, x.zero.y, x.zero.z, x.zero.w};
+  float2* sm = to.sm() + at * ng;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (4 * i >= ng) break;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (4 * i + e >= ng) break;
+      const uint32_t sb = (s[i] >> (8 * e)) & 0xFFu, zb = p.sym ? 0u : (z[i] >> (8 * e)) & 0xFFu;
+      sm[4 * i + e] = e4m3_pair(sb | (zb << 8));
+    }
+  }
+  if (TT > 0) {
+#pragma unroll
+    for (int t = 0; t < TT; ++t) to.row[t][at] = x.k[t] * (kD * 2);
+  } else if (TT < 0) {
+    for (int t = 0; t < p.T; ++t)
+      to.row[t][at] = min((uint32_t)__ldg(p.assign[w] + ((int64_t)t * p.H + h) * p.Nk + tok), (uint32_t)p.K - 1) * (kD * 2);
+  }
+}
+
+// The lane's two chunks of a token as packed bf16 pairs.
+template <int TT, int NK>
+struct Rebuild {
+  const uint8_t* tab;             // the head's first stage table, at the lane's chunk
+  int64_t tab_stage;
+  int ng, g0, g1, sym, T, c;
+
+  __device__ __forceinline__ Rebuild(const BatchParams& p, int w, int h, int lane_c) {
+    c = lane_c;
+    ng = kD >> p.lgG;
+    tab = reinterpret_cast<const uint8_t*>(p.tab[w] + (int64_t)h * p.K * kD + 8 * c);
+    tab_stage = (int64_t)p.H * p.K * kD * 2;
     g0 = (8 * c) >> p.lgG;
     g1 = (64 + 8 * c) >> p.lgG;
     sym = p.sym;
     T = TT >= 0 ? TT : p.T;
   }
-  __device__ __forceinline__ void operator()(const float2* nlut, uint32_t tok, uint4 (&out)[2]) const {
-    const uint32_t code[2] = {__ldg(reinterpret_cast<const uint16_t*>(codes + tok * 32u)),
-                              __ldg(reinterpret_cast<const uint16_t*>(codes + tok * 32u + 16u))};
-    const uint32_t at = tok << lgng;
-    uint32_t sz[2] = {__ldg(scale + at + g0), __ldg(scale + at + g1)};
-    if (!sym) {
-      sz[0] |= (uint32_t)__ldg(zero + at + g0) << 8;
-      sz[1] |= (uint32_t)__ldg(zero + at + g1) << 8;
-    }
+  __device__ __forceinline__ void operator()(const float2* nlut, const Tokens<TT, NK>& from, int at, uint4 (&out)[2]) const {
     constexpr int TR = TT > 0 ? TT : 1;
     uint4 rows[TR][2];
     if (TT > 0) {
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        const uint32_t k = min((uint32_t)__ldg(assign + t * assign_stage + tok), top);
-        const uint4* row = reinterpret_cast<const uint4*>(tab + t * tab_stage + k * (uint32_t)kD);
+        const uint4* row = reinterpret_cast<const uint4*>(tab + t * tab_stage + from.row[t][at]);
         rows[t][0] = __ldg(row);
         rows[t][1] = __ldg(row + 8);
       }
     }
+    const uint16_t* code = reinterpret_cast<const uint16_t*>(from.codes + 2 * at) + c;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float2 sm = e4m3_pair(sz[i]);
+      const float2 sm = from.sm()[at * ng + (i == 0 ? g0 : g1)];
       const float2 s2 = make_float2(sm.x, sm.x), m2 = make_float2(sm.y, sm.y);
+      const uint32_t q8 = (uint32_t)code[8 * i] << 3;             // nibbles as byte offsets into the table
       float2 y[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 q = nlut[(code[i] >> (4 * e)) & 0xFu];
+        const float2 q = *reinterpret_cast<const float2*>(reinterpret_cast<const char*>(nlut) + ((q8 >> (4 * e)) & 0x78u));
         y[e] = sym ? __fmul2_rn(s2, q) : __ffma2_rn(s2, q, m2);
       }
       auto add = [&](const uint4& v) {
@@ -92,10 +159,8 @@ struct Rebuild {
 #pragma unroll
         for (int t = TT - 1; t >= 0; --t) add(rows[t][i]);
       } else if (TT < 0) {
-        for (int t = T - 1; t >= 0; --t) {
-          const uint32_t k = min((uint32_t)__ldg(assign + t * assign_stage + tok), top);
-          add(__ldg(reinterpret_cast<const uint4*>(tab + t * tab_stage + k * (uint32_t)kD) + 8 * i));
-        }
+        for (int t = T - 1; t >= 0; --t)
+          add(__ldg(reinterpret_cast<const uint4*>(tab + t * tab_stage + from.row[t][at]) + 8 * i));
       }
       out[i] = make_uint4(pack2(y[0].x, y[0].y), pack2(y[1].x, y[1].y), pack2(y[2].x, y[2].y), pack2(y[3].x, y[3].y));
     }

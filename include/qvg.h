@@ -376,7 +376,8 @@ typedef struct {
  * all query heads of a K/V head:
  *   O[b][j][n] = softmax(rope(Q[b][j][n]) rope([K^[h]; tail_k[b][h]])^T / sqrt(d)) [V^[h]; tail_v[b][h]]
  * with h = j / group.  K^ and V^ are what qvg_dequantize would write for `k`
- * and `v` (two packed forms of H blocks of Nk tokens with the same cfg; bf16).
+ * and `v` (two packed forms of H blocks of Nk tokens with the same cfg; bf16;
+ * codes and centroids 16-byte aligned, scale and zero to d/G bytes).
  * A row that sees no key gets zeros.
  *   O  DEVICE [B][H * group][Nq][d] bf16, 16-byte aligned
  *   workspace, ws_bytes  DEVICE scratch for the partial results of the ranges

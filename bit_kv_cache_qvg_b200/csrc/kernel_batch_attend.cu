@@ -536,9 +536,14 @@ size_t attention_weights_workspace_bytes(const BatchArgs& a) {
   return plan_batch(p, false).bytes;
 }
 
-cudaError_t launch_attention_batch(const BatchArgs& a, void* O, void* ws, cudaStream_t s) {
-  BatchParams p = params_of(a);
-  const BatchPlan plan = plan_batch(p, true);
+// The tensor-core kernels record a timeout in the tables' status word; those
+// for few rows wait for nothing.
+static qvg_status ready(const BatchPlan& plan, const BatchArgs& a, size_t ws_bytes, cudaStream_t s) {
+  if (ws_bytes < plan.bytes) return QVG_ERR_WORKSPACE_TOO_SMALL;
+  return plan.tc1 || plan.tc2 ? peek_sticky(a.tables, s) : QVG_OK;
+}
+
+static cudaError_t queue_attention(const BatchPlan& plan, BatchParams& p, void* O, void* ws, cudaStream_t s) {
   place(p, plan, true, static_cast<char*>(ws));
   p.O = static_cast<__nv_bfloat16*>(O);
   cudaError_t e = cudaSuccess;
@@ -556,9 +561,7 @@ cudaError_t launch_attention_batch(const BatchArgs& a, void* O, void* ws, cudaSt
   return launch_batch_merge(p, s);
 }
 
-cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, float* out, void* ws, cudaStream_t s) {
-  BatchParams p = params_of(a);
-  const BatchPlan plan = plan_batch(p, false);
+static cudaError_t queue_weights(const BatchPlan& plan, BatchParams& p, const float* received, float* out, void* ws, cudaStream_t s) {
   place(p, plan, false, static_cast<char*>(ws));
   cudaError_t e = cudaSuccess;
   BatchParams few = share(p, plan, false);
@@ -579,6 +582,22 @@ cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, 
     if ((e = launch_batch_weights(q, p.lse, p.limits, received, out, s)) != cudaSuccess) return e;
   }
   return e;
+}
+
+qvg_status launch_attention_batch(const BatchArgs& a, void* O, void* ws, size_t ws_bytes, cudaStream_t s) {
+  BatchParams p = params_of(a);
+  const BatchPlan plan = plan_batch(p, true);
+  const qvg_status st = ready(plan, a, ws_bytes, s);
+  if (st != QVG_OK) return st;
+  return queue_attention(plan, p, O, ws, s) == cudaSuccess ? QVG_OK : QVG_ERR_CUDA;
+}
+
+qvg_status launch_attention_weights(const BatchArgs& a, const float* received, float* out, void* ws, size_t ws_bytes, cudaStream_t s) {
+  BatchParams p = params_of(a);
+  const BatchPlan plan = plan_batch(p, false);
+  const qvg_status st = ready(plan, a, ws_bytes, s);
+  if (st != QVG_OK) return st;
+  return queue_weights(plan, p, received, out, ws, s) == cudaSuccess ? QVG_OK : QVG_ERR_CUDA;
 }
 
 }  // namespace qvg

@@ -680,10 +680,7 @@ qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* k, const
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   BatchArgs a = batch_args(cfg, Nk, H, batch);
   a.k = k; a.v = v; a.tables = tables; a.max_pos = max_pos;
-  if (ws_bytes < attention_batch_workspace_bytes(a)) return QVG_ERR_WORKSPACE_TOO_SMALL;
-  st = peek_sticky(tables, s);
-  if (st != QVG_OK) return st;
-  st = cuda_status(plaunch(K_BATCH, s, [&] { return launch_attention_batch(a, O, workspace, s); }));
+  plaunch(K_BATCH, s, [&] { return (st = launch_attention_batch(a, O, workspace, ws_bytes, s)) == QVG_OK ? cudaSuccess : cudaErrorUnknown; });
   if (st == QVG_OK && fault_injected("stream")) st = QVG_ERR_CUDA;
   return st;
 }
@@ -701,10 +698,9 @@ qvg_status qvg_attention_weights(const qvg_config* cfg, const qvg_packed* k, int
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   BatchArgs a = batch_args(cfg, Nk, H, batch);
   a.k = k; a.tables = tables; a.max_pos = max_pos;
-  if (ws_bytes < attention_weights_workspace_bytes(a)) return QVG_ERR_WORKSPACE_TOO_SMALL;
-  st = peek_sticky(tables, s);
-  if (st != QVG_OK) return st;
-  st = cuda_status(plaunch(K_WEIGHTS, s, [&] { return launch_attention_weights(a, received, out, workspace, s); }));
+  plaunch(K_WEIGHTS, s, [&] {
+    return (st = launch_attention_weights(a, received, out, workspace, ws_bytes, s)) == QVG_OK ? cudaSuccess : cudaErrorUnknown;
+  });
   if (st == QVG_OK && fault_injected("stream")) st = QVG_ERR_CUDA;
   return st;
 }

@@ -181,7 +181,7 @@ int attention_split(int T, int64_t Nk, int64_t Nq, int H, int forced, size_t ws_
 size_t attention_workspace_bytes(int T, int64_t Nk, int64_t Nq, int H, int forced);
 size_t attention_smem_bytes();
 
-// ---- a batch over a shared prefix (kernel_attention_rows.cu)
+// ---- a batch over a shared prefix (kernel_batch_attend.cu)
 struct BatchArgs {
   const qvg_packed* k;         // K cache: H blocks of Nk tokens (bf16 tables)
   const qvg_packed* v;         // V cache, same configuration (null: weights)
@@ -192,10 +192,11 @@ struct BatchArgs {
   int H, K, T, G, sym;
 };
 // O [B][H * group][Nq][d] bf16.  ws: attention_batch_workspace_bytes.
-cudaError_t launch_attention_batch(const BatchArgs& a, void* O, void* ws, cudaStream_t s);
+qvg_status launch_attention_batch(const BatchArgs& a, void* O, void* ws, size_t ws_bytes, cudaStream_t s);
 size_t attention_batch_workspace_bytes(const BatchArgs& a);
 // out [H][Nk] = received (null: zeros) + the weights.  ws: attention_weights_workspace_bytes.
-cudaError_t launch_attention_weights(const BatchArgs& a, const float* received, float* out, void* ws, cudaStream_t s);
+qvg_status launch_attention_weights(const BatchArgs& a, const float* received, float* out, void* ws, size_t ws_bytes,
+                                    cudaStream_t s);
 size_t attention_weights_workspace_bytes(const BatchArgs& a);
 
 // ---- eviction (kernels_evict.cu)

@@ -389,7 +389,8 @@ typedef struct {
  * tables that do not cover Nk - 1 when k_pos is NULL), UNSUPPORTED (d != 128,
  * B * group * Nq, H * B or Nt of 2^23 or more, B * group * Nq * H of 2^31 or
  * more), WORKSPACE_TOO_SMALL, CUDA,
- * DEVICE_TIMEOUT (recorded in the tables' status word by earlier work). */
+ * DEVICE_TIMEOUT (recorded in the tables' status word by earlier work; looked
+ * at by the calls whose own kernels wait, those of more than 64 rows a head). */
 QVG_API qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* k, const qvg_packed* v, int64_t Nk,
                                int32_t H, int32_t d, const qvg_batch* batch, const void* tables,
                                size_t tables_bytes, void* O, void* workspace, size_t ws_bytes,

@@ -8,9 +8,9 @@
 // the same, bit for bit.
 //
 // Two launches:
-//   qvg_evict_select  one CTA per head: a radix select finds the weight of the
-//                     last token that is kept, then one pass in token order
-//                     writes the indices of the kept ones;
+//   qvg_evict_select  a cluster of CTAs per head: a radix select finds the
+//                     weight of the last token that is kept, then one pass in
+//                     token order writes the indices of the kept ones;
 //   qvg_evict_gather  every kept token's bytes, position and weight.
 #include "qvg_common.cuh"
 #include "qvg_launch.h"
@@ -20,7 +20,8 @@ namespace {
 
 constexpr int kEvThreads = 1024;
 constexpr int kEvBins = 2048;                     // 11 + 11 + 10 bits of a weight's order
-constexpr int kEvKeysSmem = 48 * 1024;            // weights of a head held in shared memory, at most
+constexpr int kEvKeysSmem = 48 * 1024;            // weights of a CTA held in shared memory, at most
+constexpr int kEvCluster = 8;                     // CTAs per head, at most
 constexpr int kEvTile = 128;                      // kept tokens per gather CTA
 
 // The order of the weights as unsigned integers: larger weight, larger
@@ -49,6 +50,7 @@ struct EvictParams {
   int64_t Nk, keep, first, recent;
   int H, T, ng;
   int in_smem;
+  int cluster;                    // CTAs per head
 };
 
 // Exclusive prefix sum over the CTA of two counts packed in 64 bits; *total
@@ -80,23 +82,44 @@ __device__ __forceinline__ unsigned long long block_exclusive(unsigned long long
   return base + x - v;
 }
 
-// One CTA per head.  need = keep - first - recent tokens are chosen from the
-// middle [first, Nk - recent): all whose order lies above a threshold tau,
-// and of those equal to it the first ones.  tau comes from three histograms,
-// from the highest bits down, each over the tokens that agree with the bits
-// found so far.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// two words of another CTA of the cluster, at the place of `p` in this one's
+// shared memory (8-byte aligned)
+__device__ __forceinline__ uint2 cluster_words(const uint32_t* p, uint32_t rank) {
+  uint32_t a;
+  uint2 v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// A cluster of C CTAs per head, each with a run of its tokens.  need = keep -
+// first - recent tokens are chosen from the middle [first, Nk - recent): all
+// whose order lies above a threshold tau, and of those equal to it the first
+// ones.  tau comes from three histograms, from the highest bits down, each over
+// the tokens that agree with the bits found so far; every CTA adds up the
+// cluster's through distributed shared memory and finds the same tau.
+// Latency-bound (a pass over a CTA's weights in shared memory, a barrier and a
+// scan, three times): one CTA a head took 64 us for 32 heads of 38,000 tokens.
 __global__ void __launch_bounds__(kEvThreads, 1) qvg_evict_select(const EvictParams p) {
   extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[kEvBins];
+  __shared__ __align__(8) uint32_t hist[3][kEvBins];
   __shared__ unsigned long long warp_sums[32];
   __shared__ uint32_t s_bin, s_above;
-  const int h = blockIdx.x;
+  __shared__ __align__(8) uint32_t s_counts[2];
+  const int C = p.cluster, rank = (int)(blockIdx.x % (unsigned)C), h = (int)(blockIdx.x / (unsigned)C);
   const float* w = p.weights + (int64_t)h * p.Nk;
-  const int64_t lo = p.first, hi = p.Nk - p.recent;
+  const int64_t slice = (p.Nk + C - 1) / C;
+  const int64_t from = min(rank * slice, p.Nk), to = min(from + slice, p.Nk);
+  const int64_t lo = max(p.first, from), hi = min(p.Nk - p.recent, to);      // of the middle, this CTA's
   const int64_t need = p.keep - p.first - p.recent;
-  auto order_at = [&](int64_t i) { return p.in_smem ? keys[i] : weight_order(__ldg(w + i)); };
+  auto order_at = [&](int64_t i) { return p.in_smem ? keys[i - from] : weight_order(__ldg(w + i)); };
+  for (int b = threadIdx.x; b < 3 * kEvBins; b += kEvThreads) (&hist[0][0])[b] = 0;
   if (p.in_smem)
-    for (int64_t i = lo + threadIdx.x; i < hi; i += kEvThreads) keys[i] = weight_order(__ldg(w + i));
+    for (int64_t i = lo + threadIdx.x; i < hi; i += kEvThreads) keys[i - from] = weight_order(__ldg(w + i));
+  __syncthreads();
   uint32_t tau = 0;
   int64_t left = need;                  // tokens still to be taken among those that agree with tau so far
   if (need > 0) {
@@ -105,21 +128,32 @@ __global__ void __launch_bounds__(kEvThreads, 1) qvg_evict_select(const EvictPar
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass < 2 ? 11 : 10;
       const uint32_t field = (1u << bits) - 1u;
-      for (int b = threadIdx.x; b < kEvBins; b += kEvThreads) hist[b] = 0;
-      __syncthreads();
       for (int64_t i0 = lo; i0 < hi; i0 += kEvThreads) {
         const int64_t i = i0 + threadIdx.x;
         const uint32_t o = i < hi ? order_at(i) : 0u;
         const bool in = i < hi && (o & mask) == tau;
         const uint32_t bin = in ? (o >> shift) & field : 0xFFFFFFFFu;
-        // equal weights (zeros above all) meet in one bin: one add for the lanes that agree
-        const uint32_t same = __match_any_sync(0xffffffffu, bin);
-        if (in && (int)(threadIdx.x & 31) == __ffs(same) - 1) atomicAdd(&hist[bin], (uint32_t)__popc(same));
+        // a run of equal weights (zeros above all) meets in one bin: one add for the warp
+        if (__all_sync(0xffffffffu, bin == __shfl_sync(0xffffffffu, bin, 0))) {
+          if (in && (threadIdx.x & 31) == 0) atomicAdd(&hist[pass][bin], 32u);
+        } else if (in) {
+          atomicAdd(&hist[pass][bin], 1u);
+        }
       }
-      __syncthreads();
+      if (C > 1) cluster_barrier(); else __syncthreads();
       // bins from the highest down: the first whose running count reaches `left`
       const int b1 = kEvBins - 1 - 2 * threadIdx.x, b0 = b1 - 1;
-      const unsigned long long c1 = hist[b1], c0 = hist[b0];
+      unsigned long long c1 = 0, c0 = 0;
+      if (C > 1) {
+        uint2 v[kEvCluster];
+#pragma unroll
+        for (int r = 0; r < kEvCluster; ++r) v[r] = r < C ? cluster_words(&hist[pass][b0], (uint32_t)r) : make_uint2(0u, 0u);
+#pragma unroll
+        for (int r = 0; r < kEvCluster; ++r) { c0 += v[r].x; c1 += v[r].y; }
+      } else {
+        c1 = hist[pass][b1];
+        c0 = hist[pass][b0];
+      }
       unsigned long long total;
       const unsigned long long above = block_exclusive(c1 + c0, warp_sums, &total);
       if (above < (unsigned long long)left && above + c1 + c0 >= (unsigned long long)left) {
@@ -137,9 +171,8 @@ __global__ void __launch_bounds__(kEvThreads, 1) qvg_evict_select(const EvictPar
   // `left` of the tokens equal to tau are kept, the first ones.  Every thread
   // takes a run of consecutive tokens; an odd length keeps a warp's reads of
   // shared memory in distinct banks.
-  const int64_t run = ((p.Nk + kEvThreads - 1) / kEvThreads) | 1;
-  const int64_t a = (int64_t)threadIdx.x * run < p.Nk ? (int64_t)threadIdx.x * run : p.Nk;
-  const int64_t z = a + run < p.Nk ? a + run : p.Nk;
+  const int64_t run = ((slice + kEvThreads - 1) / kEvThreads) | 1;
+  const int64_t a = min(from + (int64_t)threadIdx.x * run, to), z = min(a + run, to);
   uint32_t sure = 0, equal = 0;
   for (int64_t i = a; i < z; ++i) {
     if (i < lo || i >= hi) { ++sure; continue; }
@@ -150,7 +183,16 @@ __global__ void __launch_bounds__(kEvThreads, 1) qvg_evict_select(const EvictPar
     }
   }
   unsigned long long total;
-  const unsigned long long before = block_exclusive(((unsigned long long)sure << 32) | equal, warp_sums, &total);
+  unsigned long long before = block_exclusive(((unsigned long long)sure << 32) | equal, warp_sums, &total);
+  if (C > 1) {                          // and what the CTAs before this one hold
+    if (threadIdx.x == 0) { s_counts[0] = (uint32_t)(total >> 32); s_counts[1] = (uint32_t)total; }
+    cluster_barrier();
+    uint2 v[kEvCluster];
+#pragma unroll
+    for (int r = 0; r < kEvCluster; ++r) v[r] = r < rank ? cluster_words(s_counts, (uint32_t)r) : make_uint2(0u, 0u);
+#pragma unroll
+    for (int r = 0; r < kEvCluster; ++r) before += ((unsigned long long)v[r].x << 32) + v[r].y;
+  }
   int64_t eq = (int64_t)(before & 0xFFFFFFFFull);
   int64_t at = (int64_t)(before >> 32) + (eq < left ? eq : left);
   int32_t* out = p.kept + (int64_t)h * p.keep;
@@ -163,49 +205,66 @@ __global__ void __launch_bounds__(kEvThreads, 1) qvg_evict_select(const EvictPar
     }
     if (take) out[at++] = (int32_t)i;
   }
+  if (C > 1) cluster_barrier();         // no CTA leaves while another reads its counts
 }
 
-__device__ __forceinline__ void copy_row(const uint8_t* src, uint8_t* dst, int n) {
+// A token's d/G scale (or zero) bytes.
+__device__ __forceinline__ uint4 load_row(const uint8_t* src, int n) {
+  uint4 v = make_uint4(0, 0, 0, 0);
   switch (n) {
-    case 16: *reinterpret_cast<uint4*>(dst) = __ldg(reinterpret_cast<const uint4*>(src)); break;
-    case 8: *reinterpret_cast<uint2*>(dst) = __ldg(reinterpret_cast<const uint2*>(src)); break;
-    case 4: *reinterpret_cast<uint32_t*>(dst) = __ldg(reinterpret_cast<const uint32_t*>(src)); break;
-    case 2: *reinterpret_cast<uint16_t*>(dst) = __ldg(reinterpret_cast<const uint16_t*>(src)); break;
-    default: *dst = __ldg(src);
+    case 16: v = __ldg(reinterpret_cast<const uint4*>(src)); break;
+    case 8: { const uint2 x = __ldg(reinterpret_cast<const uint2*>(src)); v.x = x.x; v.y = x.y; break; }
+    case 4: v.x = __ldg(reinterpret_cast<const uint32_t*>(src)); break;
+    case 2: v.x = __ldg(reinterpret_cast<const uint16_t*>(src)); break;
+    default: v.x = __ldg(src);
+  }
+  return v;
+}
+__device__ __forceinline__ void store_row(uint8_t* dst, const uint4& v, int n) {
+  switch (n) {
+    case 16: *reinterpret_cast<uint4*>(dst) = v; break;
+    case 8: *reinterpret_cast<uint2*>(dst) = make_uint2(v.x, v.y); break;
+    case 4: *reinterpret_cast<uint32_t*>(dst) = v.x; break;
+    case 2: *reinterpret_cast<uint16_t*>(dst) = (uint16_t)v.x; break;
+    default: *dst = (uint8_t)v.x;
   }
 }
 
-// kEvTile kept tokens of one head: their codes (two 16-byte halves), scale
-// and zero rows (d/G bytes), centroid indices, positions and weights.
-__global__ void __launch_bounds__(256) qvg_evict_gather(const EvictParams p) {
-  __shared__ int32_t from[kEvTile];
-  const int h = blockIdx.y;
-  const int64_t i0 = (int64_t)blockIdx.x * kEvTile;
-  const int n = (int)(p.keep - i0 < kEvTile ? p.keep - i0 : kEvTile);
-  const int64_t in0 = (int64_t)h * p.Nk, out0 = (int64_t)h * p.keep + i0;
-  if (threadIdx.x < n) {
-    const int32_t f = __ldg(p.kept + out0 + threadIdx.x);
-    from[threadIdx.x] = f;
-    if (p.pos_out != nullptr) p.pos_out[out0 + threadIdx.x] = p.k_pos != nullptr ? __ldg(p.k_pos + in0 + f) : (int64_t)f;
-    if (p.weights_out != nullptr) p.weights_out[out0 + threadIdx.x] = __ldg(p.weights + in0 + f);
-  }
-  __syncthreads();
+// kEvTile kept tokens of one head, two threads to a token: each moves a half of
+// both caches' codes and one cache's scales, zero points and centroid indices,
+// and one of them the position, the other the weight.  Everything a thread reads
+// is on its way before it writes: stores between the loads made a chain of a
+// dozen memory latencies of it.
+__global__ void __launch_bounds__(2 * kEvTile) qvg_evict_gather(const EvictParams p) {
+  const int h = blockIdx.y, side = threadIdx.x & 1;
+  const int64_t i = (int64_t)blockIdx.x * kEvTile + (threadIdx.x >> 1);
+  if (i >= p.keep) return;
+  const int64_t out = (int64_t)h * p.keep + i;
+  const int32_t f = __ldg(p.kept + out);
+  const int64_t in = (int64_t)h * p.Nk + f;
+  uint4 codes[2];
 #pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    for (int e = threadIdx.x; e < 2 * n; e += 256) {
-      const int i = e >> 1, half = e & 1;
-      reinterpret_cast<uint4*>(p.codes_out[c])[2 * (out0 + i) + half] =
-          __ldg(reinterpret_cast<const uint4*>(p.codes[c]) + 2 * (in0 + from[i]) + half);
-    }
-    for (int i = threadIdx.x; i < n; i += 256) {
-      copy_row(p.scale[c] + (in0 + from[i]) * p.ng, p.scale_out[c] + (out0 + i) * p.ng, p.ng);
-      if (p.zero[c] != nullptr) copy_row(p.zero[c] + (in0 + from[i]) * p.ng, p.zero_out[c] + (out0 + i) * p.ng, p.ng);
-    }
-    for (int e = threadIdx.x; e < p.T * n; e += 256) {
-      const int t = e / n, i = e - t * n;
-      p.assign_out[c][(int64_t)t * p.H * p.keep + out0 + i] = __ldg(p.assign[c] + (int64_t)t * p.H * p.Nk + in0 + from[i]);
-    }
-  }
+  for (int c = 0; c < 2; ++c) codes[c] = __ldg(reinterpret_cast<const uint4*>(p.codes[c]) + 2 * in + side);
+  const uint4 scale = load_row(p.scale[side] + in * p.ng, p.ng);
+  uint4 zero = make_uint4(0, 0, 0, 0);
+  if (p.zero[side] != nullptr) zero = load_row(p.zero[side] + in * p.ng, p.ng);
+  uint8_t assign[kMaxT];
+#pragma unroll
+  for (int t = 0; t < kMaxT; ++t)
+    if (t < p.T) assign[t] = __ldg(p.assign[side] + (int64_t)t * p.H * p.Nk + in);
+  int64_t pos = f;
+  float weight = 0.0f;
+  if (side == 0 && p.pos_out != nullptr && p.k_pos != nullptr) pos = __ldg(p.k_pos + in);
+  if (side == 1 && p.weights_out != nullptr) weight = __ldg(p.weights + in);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) reinterpret_cast<uint4*>(p.codes_out[c])[2 * out + side] = codes[c];
+  store_row(p.scale_out[side] + out * p.ng, scale, p.ng);
+  if (p.zero[side] != nullptr) store_row(p.zero_out[side] + out * p.ng, zero, p.ng);
+#pragma unroll
+  for (int t = 0; t < kMaxT; ++t)
+    if (t < p.T) p.assign_out[side][(int64_t)t * p.H * p.keep + out] = assign[t];
+  if (side == 0 && p.pos_out != nullptr) p.pos_out[out] = pos;
+  if (side == 1 && p.weights_out != nullptr) p.weights_out[out] = weight;
 }
 
 }  // namespace
@@ -223,16 +282,33 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   }
   p.Nk = a.Nk; p.keep = a.keep; p.first = a.first; p.recent = a.recent;
   p.H = a.H; p.T = a.T; p.ng = kD / a.G;
-  p.in_smem = a.Nk <= kEvKeysSmem ? 1 : 0;
-  const size_t smem = p.in_smem ? (size_t)a.Nk * sizeof(uint32_t) : 0;
-  // the histogram's static shared memory counts towards the 48 KB that need no attribute
+  // CTAs for a head: a power of two up to the portable cluster size, as long as
+  // the heads leave SMs idle and a CTA has a few thousand tokens
+  p.cluster = 1;
+  while (p.cluster < kEvCluster && 2 * p.cluster * p.H <= device_sm_count() && p.Nk >= 2 * p.cluster * 2048) p.cluster *= 2;
+  const int64_t slice = (a.Nk + p.cluster - 1) / p.cluster;
+  p.in_smem = slice <= kEvKeysSmem ? 1 : 0;
+  const size_t smem = p.in_smem ? (size_t)slice * sizeof(uint32_t) : 0;
+  // the histograms' static shared memory counts towards the 48 KB that need no attribute
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(qvg_evict_select),
-                                      smem > 32 * 1024 ? kEvKeysSmem * sizeof(uint32_t) : 0);
+                                      smem > 16 * 1024 ? kEvKeysSmem * sizeof(uint32_t) : 0);
   if (e != cudaSuccess) return e;
-  qvg_evict_select<<<(unsigned)a.H, kEvThreads, smem, s>>>(p);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.H * p.cluster));
+  cfg.blockDim = dim3(kEvThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)p.cluster;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+  if ((e = cudaLaunchKernelEx(&cfg, qvg_evict_select, p)) != cudaSuccess) return e;
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const dim3 grid((unsigned)((a.keep + kEvTile - 1) / kEvTile), (unsigned)a.H);
-  qvg_evict_gather<<<grid, 256, 0, s>>>(p);
+  qvg_evict_gather<<<grid, 2 * kEvTile, 0, s>>>(p);
   return cudaGetLastError();
 }
 

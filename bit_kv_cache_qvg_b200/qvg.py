@@ -524,10 +524,15 @@ class Evicted:
 
 def _closed(p: Packed, keep: int) -> Packed:
     """Streams for `keep` tokens a head beside p's own centroid tables."""
-    ng, H = p.d // p.cfg.group_size, p.H
-    new = p.codes.new_empty
-    return Packed(codes=new((H, keep, p.d // 4)), scale=new((H, keep, ng)),
-                  zero=new((H, keep, ng) if p.cfg.scale_mode == ASYM else (0,)), assign=new((p.cfg.T, H, keep)),
+    ng, H, T = p.d // p.cfg.group_size, p.H, p.cfg.T
+    # one allocation, each stream from a 256-byte boundary
+    shapes = [(H, keep, p.d // 4), (H, keep, ng), (H, keep, ng) if p.cfg.scale_mode == ASYM else (0, keep, ng), (T, H, keep)]
+    at = [0]
+    for a, b, c in shapes:
+        at.append(at[-1] + (a * b * c + 255) // 256 * 256)
+    buf = p.codes.new_empty(at[-1])
+    codes, scale, zero, assign = (buf.as_strided(s, (s[1] * s[2], s[2], 1), o) for s, o in zip(shapes, at))
+    return Packed(codes=codes, scale=scale, zero=zero if p.cfg.scale_mode == ASYM else p.zero, assign=assign,
                   centroids=p.centroids, cfg=p.cfg, N=keep, H=H, d=p.d, dtype=p.dtype)
 
 

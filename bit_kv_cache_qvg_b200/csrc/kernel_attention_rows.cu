@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchP
     uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
     if (a.r0 + r < a.r1) {
       const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.Q + query_row(p, a.h, a.r0 + r) * kD + 8 * cb));
-      turn_chunk<!VALUES>(reinterpret_cast<const float4*>(p.rope + rope_row(p, query_pos(p, a.r0 + r)) * (kD / 2) + 4 * cb), x, hi, lo);
+      turn_chunk<!VALUES>(p.rope + rope_row(p, query_pos(p, a.r0 + r)) * (kD / 2) + 4 * cb, x, hi, lo);
     }
     *reinterpret_cast<uint4*>(sQ + r * kRwPitch + 8 * cb) = hi;
     if (!VALUES) *reinterpret_cast<uint4*>(sQ + (kRows + r) * kRwPitch + 8 * cb) = lo;
@@ -183,10 +183,10 @@ __global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchP
           }
         }
       }
-      const float4* cs = reinterpret_cast<const float4*>(p.rope + (int64_t)turn[at] * (kD / 2) + 4 * rc);
+      const float2* cs = p.rope + (int64_t)turn[at] * (kD / 2) + 4 * rc;
       uint4 hi[2], lo[2];
       turn_chunk<!VALUES>(cs, x[0], hi[0], lo[0]);
-      turn_chunk<!VALUES>(cs + 16, x[1], hi[1], lo[1]);
+      turn_chunk<!VALUES>(cs + 32, x[1], hi[1], lo[1]);
       __nv_bfloat16* dk = sK + at * kRwPitch + 8 * rc;
       *reinterpret_cast<uint4*>(dk) = hi[0];
       *reinterpret_cast<uint4*>(dk + 64) = hi[1];

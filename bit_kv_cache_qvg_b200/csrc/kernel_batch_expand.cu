@@ -38,7 +38,7 @@ __device__ __forceinline__ void expand_rows(const BatchParams& p, bool by_sequen
     if (r < rows) {
       const int64_t row = by_sequence ? b * p.RB + r : r;
       const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.Q + query_row(p, p.h0 + hl, row) * kD + 8 * cb));
-      turn_chunk<PRECISE>(reinterpret_cast<const float4*>(p.rope + rope_row(p, query_pos(p, row)) * (kD / 2) + 4 * cb), x, hi, lo);
+      turn_chunk<PRECISE>(p.rope + rope_row(p, query_pos(p, row)) * (kD / 2) + 4 * cb, x, hi, lo);
     }
     const int64_t at = (base + (cb >> 3) * pad + r) * 128 + (((cb & 7) ^ (int)(r & 7)) << 4);
     *reinterpret_cast<uint4*>(p.row_img[which] + at) = hi;
@@ -82,10 +82,10 @@ __device__ __forceinline__ void expand_tile(const BatchParams& p, uint8_t* smem,
       *reinterpret_cast<uint4*>(dst + kAtHalfBytes) = x[1];
       return;
     }
-    const float4* cs = reinterpret_cast<const float4*>(p.rope + (int64_t)turn[pass * kExKeys + key0] * (kD / 2) + 4 * c);
+    const float2* cs = p.rope + (int64_t)turn[pass * kExKeys + key0] * (kD / 2) + 4 * c;
     uint4 hi[2], lo[2];
     turn_chunk<PRECISE>(cs, x[0], hi[0], lo[0]);
-    turn_chunk<PRECISE>(cs + 16, x[1], hi[1], lo[1]);
+    turn_chunk<PRECISE>(cs + 32, x[1], hi[1], lo[1]);
     *reinterpret_cast<uint4*>(dst) = hi[0];
     *reinterpret_cast<uint4*>(dst + kAtHalfBytes) = hi[1];
     if (PRECISE) {

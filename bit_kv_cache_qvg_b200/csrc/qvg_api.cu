@@ -639,7 +639,7 @@ static qvg_status check_batch_pointers(const qvg_batch* b, int64_t Nk, bool valu
   if (b->Nt > 0 && (b->tail_k == nullptr || !aligned(b->tail_k, 16) || !aligned(b->tail_pos, 8) || !aligned(b->tail_len, 4) ||
                     (values && (b->tail_v == nullptr || !aligned(b->tail_v, 16)))))
     return QVG_ERR_INVALID_ARG;
-  if (tables == nullptr || !aligned(tables, 16) || workspace == nullptr || !aligned(workspace, 16) ||
+  if (tables == nullptr || !aligned(tables, 32) || workspace == nullptr || !aligned(workspace, 16) ||
       tables_bytes < kRopeHeaderBytes + kRopeRowBytes)
     return QVG_ERR_INVALID_ARG;
   *max_pos = std::min<int64_t>((int64_t)((tables_bytes - kRopeHeaderBytes) / kRopeRowBytes), kRopeMaxPositions) - 1;

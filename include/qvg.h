@@ -379,6 +379,7 @@ typedef struct {
  * and `v` (two packed forms of H blocks of Nk tokens with the same cfg; bf16;
  * codes and centroids 16-byte aligned, scale and zero to d/G bytes).
  * A row that sees no key gets zeros.
+ *   tables  DEVICE rotary tables (qvg_rope_tables), 32-byte aligned
  *   O  DEVICE [B][H * group][Nq][d] bf16, 16-byte aligned
  *   workspace, ws_bytes  DEVICE scratch for the partial results of the ranges
  *      that the keys are cut into, 16-byte aligned, not shared with calls

@@ -7,12 +7,17 @@
 // All rows of a K/V head (every sequence, every query head of the group) read
 // the same prefix: a CTA takes up to 64 of them and a range of the keys, 64 at a
 // time.  Its four warps rebuild the 64 keys and values into shared memory
-// (eight lanes to a token, as kernel_batch_expand.cu), then multiply:
-// mma.sync m16n8k16 with bf16 operands and fp32 sums, a warp having 16 rows and
-// as many of the 64 keys as leave no warp idle, with a running maximum and sum
-// of its own.  With few rows the rebuilding is the bound, about 60 instructions
-// a token and cache; small CTAs, four to an SM, overlap one's products with
+// (rebuild.cuh), then multiply: mma.sync m16n8k16 with bf16 operands and fp32
+// sums.  For the scores a warp has 16 rows and as many of the 64 keys as leave
+// no warp idle; the weights go through shared memory, and for O a warp has 32
+// channels of all rows, so that its sums take few registers.  The weights are
+// taken against a reference that the warps share and that rises only when a
+// row's maximum exceeds it by more than 8 (base 2).  With few rows the
+// rebuilding is the bound, and with it the latency of the centroid rows and
+// the rotary table: small CTAs, five to an SM, overlap one's products with
 // another's loads.
+#include <algorithm>
+
 #include "batch.cuh"
 #include "rebuild.cuh"
 
@@ -21,6 +26,7 @@ namespace {
 
 constexpr int kRwThreads = 128;                   // 4 warps
 constexpr int kRwKeys = 64;                       // keys per CTA and step
+constexpr int kRwPPitch = kRwKeys + 8;            // the same for the weights
 constexpr int kRwPitch = kD + 8;                  // padded row in shared memory (bf16): ldmatrix meets no bank twice
 
 // D += A B, m16n8k16, bf16 operands
@@ -74,7 +80,7 @@ __device__ __forceinline__ Place place_of(const BatchParams& p, int rows_per_cta
 // from operands of two bf16 halves (three products: high x high, low x high,
 // high x low), so that they are good to fp32.
 template <int TT, int MT, bool VALUES>
-__global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchParams p) {
+__global__ void __launch_bounds__(kRwThreads, MT == 4 || !VALUES ? 4 : 5) qvg_attention_rows(const BatchParams p) {
   constexpr int kRows = 16 * MT;
   constexpr int kWarpKeys = 16 * MT;              // of a step's 64
   constexpr int kTiles = kWarpKeys / 8;           // tiles of 8 keys of a warp
@@ -83,12 +89,15 @@ __global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchP
   __nv_bfloat16* sV = sK + kRwKeys * kRwPitch;                       // values, or the keys' low halves
   __nv_bfloat16* sQ = sV + kRwKeys * kRwPitch;                       // rows (high halves, then low)
   float2* nlut = reinterpret_cast<float2*>(sQ + (VALUES ? 1 : 2) * kRows * kRwPitch);
-  float2* sml = nlut + 16;                                           // [4][16]: a warp's rows at the end
-  int* spos = reinterpret_cast<int*>(sml + 64);                      // [2][64]: positions for the masks, by step
+  float2* sml = nlut + 16;                                           // [4][16]: a warp's rows: maxima, at the end sums
+  float* sref = reinterpret_cast<float*>(sml + 64);                  // [64]: 2^(old - new) of a raised reference, by row
+  int* sflag = reinterpret_cast<int*>(sref + 64);                    // [4]: a warp has a row that asks for it
+  int* spos = sflag + 4;                                            // [2][64]: positions for the masks, by step
   uint32_t* turn = reinterpret_cast<uint32_t*>(spos + 2 * kRwKeys);  // rows of the rotary table
   using Block = Tokens<TT, kRwKeys>;
   Block& tk = *reinterpret_cast<Block*>(turn + kRwKeys);
   Block& tv = *reinterpret_cast<Block*>(reinterpret_cast<uint8_t*>(&tk) + Block::bytes(kD >> p.lgG));
+  __nv_bfloat16* sP = reinterpret_cast<__nv_bfloat16*>(reinterpret_cast<uint8_t*>(&tv) + Block::bytes(kD >> p.lgG));   // weights
   const Place a = place_of(p, kRows);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const int mt = warp % MT, kg = warp / MT;       // the warp's rows and keys
@@ -111,12 +120,14 @@ __global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchP
     limit[i] = r < a.r1 ? row_limit(p, query_pos(p, r)) : kLimitNone;
   }
   float m[2] = {kNoMax, kNoMax}, l[2] = {0.0f, 0.0f};
-  float o[VALUES ? 16 : 1][4];
+  float o[VALUES ? MT : 1][4][4];                 // O of all rows and channels 32 warp .. + 31
   if (VALUES) {
 #pragma unroll
-    for (int n = 0; n < 16; ++n)
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[t][n][e] = 0.0f;
   }
   // rebuilding: the lane's key of a pass and its chunks rc and rc + 8
   const int rc = threadIdx.x & 7, rkey = threadIdx.x >> 3;
@@ -153,7 +164,8 @@ __global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchP
   // ldmatrix: a warp's rows of Q, 8 keys of K (four 8 x 8 tiles along the channels), 16 keys of V
   const uint32_t aQ = shared_addr(sQ + (16 * mt + (lane & 15)) * kRwPitch + 8 * (lane >> 4));
   const uint32_t aK = shared_addr(sK + (kWarpKeys * kg + (lane & 7)) * kRwPitch + 8 * (lane >> 3));
-  const uint32_t aV = shared_addr(sV + (kWarpKeys * kg + (lane & 15)) * kRwPitch + 8 * (lane >> 4));
+  const uint32_t aV = shared_addr(sV + (lane & 15) * kRwPitch + 32 * warp + 8 * (lane >> 4));
+  const uint32_t aP = shared_addr(sP + (lane & 15) * kRwPPitch + 8 * (lane >> 4));
   constexpr uint32_t kLow = kRwKeys * kRwPitch * 2;          // from the keys' high halves to the low ones
   if (a.k0 < a.k1) fetch(a.k0);
   int parity = 0;
@@ -244,51 +256,90 @@ __global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchP
         }
       }
     }
-    float alpha[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
       top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-      const float mn = fmaxf(m[i], top[i]);
-      alpha[i] = ex2(m[i] - mn);
-      m[i] = mn;
-      l[i] *= alpha[i];
     }
     if (VALUES) {
-      if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f)) {
+      // weights against the reference, of 16 rows x kWarpKeys keys
+      float add[2];
+      auto weigh = [&] {
+        add[0] = add[1] = 0.0f;
 #pragma unroll
-        for (int n = 0; n < 16; ++n) {
-          o[n][0] *= alpha[0]; o[n][1] *= alpha[0];
-          o[n][2] *= alpha[1]; o[n][3] *= alpha[1];
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < kTiles; t += 2) {        // 16 keys: two score tiles are one operand
-        uint32_t pa[4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int t = 0; t < kTiles; ++t)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t w = pack2(ex2(s[t + u][2 * i] - m[i]), ex2(s[t + u][2 * i + 1] - m[i]));
-            pa[2 * u + i] = w;
-            l[i] += lo_f(w) + hi_f(w);             // of the rounded weights, the ones the product uses
+            const uint32_t x = pack2(ex2(s[t][2 * i] - m[i]), ex2(s[t][2 * i + 1] - m[i]));
+            add[i] += lo_f(x) + hi_f(x);           // of the rounded weights, the ones the product uses
+            *reinterpret_cast<uint32_t*>(sP + (16 * mt + g + 8 * i) * kRwPPitch + kWarpKeys * kg + 8 * t + 2 * c) = x;
           }
+      };
+      weigh();
+      const bool raise = __any_sync(0xffffffffu, top[0] > m[0] + 8.0f || top[1] > m[1] + 8.0f);
+      if (lane == 0) sflag[warp] = raise;
+      __syncthreads();
+      const int4 flags = *reinterpret_cast<const int4*>(sflag);
+      if (flags.x | flags.y | flags.z | flags.w) {
+        // the reference rises to the rows' maxima: weights again, sums and O rescaled
+        if (c == 0) { sml[warp * 16 + g].x = top[0]; sml[warp * 16 + g + 8].x = top[1]; }
+        __syncthreads();
 #pragma unroll
-        for (int n = 0; n < 8; ++n) {
-          uint32_t b[4];
-          ldm4t(aV + t * 8 * kRwPitch * 2 + n * 32, b);
-          mma16816(o[2 * n], pa, b[0], b[1]);
-          mma16816(o[2 * n + 1], pa, b[2], b[3]);
+        for (int i = 0; i < 2; ++i) {
+          float mn = m[i];
+#pragma unroll
+          for (int w2 = 0; w2 < 4 / MT; ++w2) mn = fmaxf(mn, sml[(mt + w2 * MT) * 16 + g + 8 * i].x);
+          const float f = ex2(m[i] - mn);
+          if (kg == 0 && c == 0) sref[16 * mt + g + 8 * i] = f;
+          l[i] *= f;
+          m[i] = mn;
+        }
+        weigh();
+        __syncthreads();
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          const float f0 = sref[16 * t + g], f1 = sref[16 * t + g + 8];
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            o[t][n][0] *= f0; o[t][n][1] *= f0;
+            o[t][n][2] *= f1; o[t][n][3] *= f1;
+          }
+        }
+      }
+      l[0] += add[0];
+      l[1] += add[1];
+      // O of all rows and the warp's 32 channels
+#pragma unroll
+      for (int k = 0; k < kRwKeys / 16; ++k) {
+        uint32_t b[2][4];
+        ldm4t(aV + k * 16 * kRwPitch * 2, b[0]);
+        ldm4t(aV + k * 16 * kRwPitch * 2 + 32, b[1]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          uint32_t pa[4];
+          ldm4(aP + (t * 16 * kRwPPitch + k * 16) * 2, pa);
+          mma16816(o[t][0], pa, b[0][0], b[0][1]);
+          mma16816(o[t][1], pa, b[0][2], b[0][3]);
+          mma16816(o[t][2], pa, b[1][0], b[1][1]);
+          mma16816(o[t][3], pa, b[1][2], b[1][3]);
         }
       }
     } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mn = fmaxf(m[i], top[i]);
+        l[i] *= ex2(m[i] - mn);
+        m[i] = mn;
+      }
 #pragma unroll
       for (int t = 0; t < kTiles; ++t)
 #pragma unroll
         for (int i = 0; i < 2; ++i) l[i] += ex2(s[t][2 * i] - m[i]) + ex2(s[t][2 * i + 1] - m[i]);
     }
   }
-  // the results of the warps with the same rows joined
+  // the sums of the warps with the same rows joined (with VALUES their
+  // references are equal), and O
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
@@ -296,44 +347,32 @@ __global__ void __launch_bounds__(kRwThreads, 4) qvg_attention_rows(const BatchP
     if (c == 0) sml[warp * 16 + g + 8 * i] = make_float2(m[i], l[i]);
   }
   __syncthreads();
-  float f[2];
+  if (kg == 0 && c == 0) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float M = kNoMax, L = 0.0f;
+    for (int i = 0; i < 2; ++i) {
+      float M = kNoMax, L = 0.0f;
 #pragma unroll
-    for (int w = 0; w < 4 / MT; ++w) M = fmaxf(M, sml[(mt + w * MT) * 16 + g + 8 * i].x);
+      for (int w2 = 0; w2 < 4 / MT; ++w2) M = fmaxf(M, sml[(mt + w2 * MT) * 16 + g + 8 * i].x);
 #pragma unroll
-    for (int w = 0; w < 4 / MT; ++w) {
-      const float2 x = sml[(mt + w * MT) * 16 + g + 8 * i];
-      L += x.y * ex2(x.x - M);
+      for (int w2 = 0; w2 < 4 / MT; ++w2) {
+        const float2 x = sml[(mt + w2 * MT) * 16 + g + 8 * i];
+        L += x.y * ex2(x.x - M);
+      }
+      const int r = a.r0 + 16 * mt + g + 8 * i;
+      if (r < a.r1) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + r] = make_float2(M, L);
     }
-    f[i] = ex2(m[i] - M);
-    const int r = a.r0 + 16 * mt + g + 8 * i;
-    if (kg == 0 && c == 0 && r < a.r1) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + r] = make_float2(M, L);
   }
   if (VALUES) {
-    constexpr int ST = kD + 4;
-    float* sO = reinterpret_cast<float*>(smem);    // over K and V
-    for (int w = 0; w < 4 / MT; ++w) {
-      if (kg == w) {
 #pragma unroll
-        for (int n = 0; n < 16; ++n)
+    for (int t = 0; t < MT; ++t)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float2* d = reinterpret_cast<float2*>(sO + (16 * mt + g + 8 * i) * ST + 8 * n + 2 * c);
-            float2 x = make_float2(o[n][2 * i] * f[i], o[n][2 * i + 1] * f[i]);
-            if (w > 0) { x.x += d->x; x.y += d->y; }
-            *d = x;
-          }
+      for (int i = 0; i < 2; ++i) {
+        const int r = a.r0 + 16 * t + g + 8 * i;
+        if (r >= a.r1) continue;
+        float* row = p.part_O + (((int64_t)a.slot * p.H + a.h) * p.R + r) * kD + 32 * warp + 2 * c;
+#pragma unroll
+        for (int n = 0; n < 4; ++n) *reinterpret_cast<float2*>(row + 8 * n) = make_float2(o[t][n][2 * i], o[t][n][2 * i + 1]);
       }
-      __syncthreads();
-    }
-    for (int e = threadIdx.x; e < kRows * kD / 4; e += kRwThreads) {
-      const int r = e >> 5, c4 = e & 31;
-      if (a.r0 + r < a.r1)
-        reinterpret_cast<float4*>(p.part_O + (((int64_t)a.slot * p.H + a.h) * p.R + a.r0 + r) * kD)[c4] =
-            *reinterpret_cast<const float4*>(sO + r * ST + 4 * c4);
-    }
   }
 }
 
@@ -430,7 +469,8 @@ __global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p) {
 size_t rows_smem(int T, int G, int mt, bool values) {
   const size_t tiles = (size_t)(2 * kRwKeys + (values ? 1 : 2) * 16 * mt) * kRwPitch * 2;
   const size_t block = kRwKeys * (32 + sizeof(uint32_t) * (T >= 0 && T <= 4 ? (T > 0 ? T : 1) : kMaxT) + kD / G * sizeof(float2));
-  return tiles + (16 + 64) * sizeof(float2) + 3 * kRwKeys * sizeof(int) + (values ? 2 : 1) * block;
+  return tiles + (16 + 64) * sizeof(float2) + (64 + 4 + 3 * kRwKeys) * sizeof(int) + (values ? 2 : 1) * block +
+         (values ? (size_t)16 * mt * kRwPPitch * 2 : 0);
 }
 
 template <int TT, int MT, bool VALUES>
@@ -465,12 +505,12 @@ cudaError_t launch_rows(const BatchParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs to an SM: four by their registers, fewer where the rows or small groups
-// need more shared memory.
+// CTAs to an SM: five (or four) by their registers, fewer where the rows or
+// small groups need more shared memory.
 int rows_per_sm(const BatchParams& p, bool values) {
   const size_t smem = rows_smem(p.T, p.G, p.row_tiles, values) + 1024;
   const int n = (int)(size_t(228 * 1024) / smem);
-  return n < 4 ? n : 4;
+  return std::min(n, values && p.row_tiles < 4 ? 5 : 4);
 }
 
 cudaError_t launch_rows_partial(const BatchParams& p, bool values, cudaStream_t s) {

@@ -63,6 +63,8 @@ constexpr int64_t kImageBytes = 128 * kD * 2;     // one 128 x 128 bf16 operand 
 
 cudaError_t launch_rows_partial(const BatchParams& p, bool values, cudaStream_t s);      // kernel_attention_rows.cu
 int rows_per_sm(const BatchParams& p, bool values);
+cudaError_t launch_single_partial(const BatchParams& p, bool values, cudaStream_t s);    // kernel_attention_single.cu
+int single_per_sm(const BatchParams& p, bool values);
 cudaError_t launch_rows_weights(const BatchParams& p, const float* received, float* out, cudaStream_t s);
 cudaError_t launch_batch_merge(const BatchParams& p, cudaStream_t s);
 cudaError_t launch_batch_expand(const BatchParams& p, bool precise, cudaStream_t s);     // kernel_batch_expand.cu

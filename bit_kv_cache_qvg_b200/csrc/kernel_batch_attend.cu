@@ -374,6 +374,8 @@ cudaError_t launch_batch_attend(const BatchParams& p, cudaStream_t s) {
 namespace {
 
 constexpr int kRowStep = 64;                      // keys of a step of the kernels for few rows
+constexpr int kSingleStep = 32;                   // and of one or two rows
+constexpr int64_t kSingleRows = 2;
 constexpr int64_t kManyRows = 64;                 // rows beyond which tcgen05 takes over
 constexpr int64_t kFewMaxRanges = 64;              // ranges of few rows
 constexpr size_t kImageBudget = size_t(1) << 30;  // operand tiles in the workspace at a time, about
@@ -419,6 +421,7 @@ struct BatchPlan {
   bool tc1, tc2;                  // prefix, tails
   int S1, S2, Hn;                 // ranges; heads at a time
   int row_tiles;
+  bool single;                    // one or two rows: kernel_attention_single.cu
   size_t bytes;
 };
 
@@ -471,9 +474,10 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
   const int64_t few = plan.tc1 ? p.RB : p.R;       // rows of the CTAs of the kernels for few rows
   plan.row_tiles = few <= 16 ? 1 : few <= 32 ? 2 : 4;
   p.row_tiles = plan.row_tiles;
-  const int64_t tile = 16 * plan.row_tiles, room = (int64_t)sms * rows_per_sm(p, values);
-  const int64_t steps1 = plan.tc1 ? 0 : (p.Nk + kRowStep - 1) / kRowStep;
-  const int64_t steps2 = plan.tc2 ? 0 : (p.Nt + kRowStep - 1) / kRowStep;
+  plan.single = p.R <= kSingleRows;
+  const int64_t tile = 16 * plan.row_tiles, step = plan.single ? kSingleStep : kRowStep;
+  const int64_t room = (int64_t)sms * (plan.single ? single_per_sm(p, values) : rows_per_sm(p, values));
+  const int64_t steps1 = plan.tc1 ? 0 : (p.Nk + step - 1) / step, steps2 = plan.tc2 ? 0 : (p.Nt + step - 1) / step;
   if (!plan.tc1 && !values)
     plan.Hn = (int)std::max<int64_t>(1, std::min<int64_t>(p.H, (int64_t)(kImageBudget / ((size_t)p.R * p.Nkp * sizeof(float)))));
   if (steps1 + steps2 > 0) {
@@ -509,6 +513,11 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
   }
   plan.bytes = place(p, plan, values, nullptr);
   return plan;
+}
+
+// Partial results of few rows.
+cudaError_t launch_few(const BatchPlan& plan, const BatchParams& p, bool values, cudaStream_t s) {
+  return plan.single ? launch_single_partial(p, values, s) : launch_rows_partial(p, values, s);
 }
 
 // The launch's share of the plan: what the kernels for few rows take, or the
@@ -548,7 +557,7 @@ static cudaError_t queue_attention(const BatchPlan& plan, BatchParams& p, void* 
   p.O = static_cast<__nv_bfloat16*>(O);
   cudaError_t e = cudaSuccess;
   const BatchParams few = share(p, plan, false);
-  if (few.S1 + few.S2 > 0 && (e = launch_rows_partial(few, true, s)) != cudaSuccess) return e;
+  if (few.S1 + few.S2 > 0 && (e = launch_few(plan, few, true, s)) != cudaSuccess) return e;
   if (plan.tc1) {
     BatchParams q = share(p, plan, true);
     for (q.h0 = 0; q.h0 < p.H; q.h0 += plan.Hn) {
@@ -568,12 +577,12 @@ static cudaError_t queue_weights(const BatchPlan& plan, BatchParams& p, const fl
   if (!plan.tc1) {
     for (few.h0 = 0; few.h0 < p.H; few.h0 += plan.Hn) {
       few.Hn = std::min(plan.Hn, p.H - few.h0);
-      if ((e = launch_rows_partial(few, false, s)) != cudaSuccess) return e;
+      if ((e = launch_few(plan, few, false, s)) != cudaSuccess) return e;
       if ((e = launch_rows_weights(few, received, out, s)) != cudaSuccess) return e;
     }
     return e;
   }
-  if (few.S2 > 0 && (e = launch_rows_partial(few, false, s)) != cudaSuccess) return e;
+  if (few.S2 > 0 && (e = launch_few(plan, few, false, s)) != cudaSuccess) return e;
   BatchParams q = share(p, plan, true);
   for (q.h0 = 0; q.h0 < p.H; q.h0 += plan.Hn) {
     q.Hn = std::min(plan.Hn, p.H - q.h0);

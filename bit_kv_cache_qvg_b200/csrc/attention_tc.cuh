@@ -353,7 +353,15 @@ __device__ __forceinline__ bool elect_one() {
 }
 template <class T>
 __device__ __forceinline__ T uniform(T x) { return __shfl_sync(0xffffffffu, x, 0); }
-// D += A B with A in tensor memory, as mma_ta, for another instruction descriptor
+// D += A B as mma and mma_ta, for another instruction descriptor
+__device__ __forceinline__ void mma_as(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 __device__ __forceinline__ void mma_ta_as(uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
@@ -362,6 +370,7 @@ __device__ __forceinline__ void mma_ta_as(uint32_t tmem_d, uint32_t tmem_a, uint
       "r"(tmem_a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+constexpr uint32_t kIdescScores = kIdesc & ~((7u << 7) | (7u << 10));   // A = B = f16
 // The steps of an operand tile's descriptor: K-step kk (16 columns) of a K-major one.
 __device__ __forceinline__ uint64_t desc_step(int kk) {
   return (uint64_t)((kk >> 2) * (kAtHalfBytes >> 4) + (kk & 3) * 2);

@@ -7,8 +7,8 @@
 // All rows of a K/V head (every sequence, every query head of the group) read
 // the same prefix: a CTA takes up to 64 of them and a range of the keys, 64 at a
 // time.  Its four warps rebuild the 64 keys and values into shared memory
-// (rebuild.cuh), then multiply: mma.sync m16n8k16 with bf16 operands and fp32
-// sums.  For the scores a warp has 16 rows and as many of the 64 keys as leave
+// (rebuild.cuh), then multiply: mma.sync m16n8k16, fp16 operands for the scores
+// and bf16 for O, fp32 sums.  For the scores a warp has 16 rows and as many of the 64 keys as leave
 // no warp idle; the weights go through shared memory, and for O a warp has 32
 // channels of all rows, so that its sums take few registers.  The weights are
 // taken against a reference that the warps share and that rises only when a
@@ -29,8 +29,14 @@ constexpr int kRwKeys = 64;                       // keys per CTA and step
 constexpr int kRwPPitch = kRwKeys + 8;            // the same for the weights
 constexpr int kRwPitch = kD + 8;                  // padded row in shared memory (bf16): ldmatrix meets no bank twice
 
-// D += A B, m16n8k16, bf16 operands
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+// D += A B, m16n8k16: fp16 operands for the scores, bf16 for O
+__device__ __forceinline__ void mma_scores(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_values(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -77,7 +83,7 @@ __device__ __forceinline__ Place place_of(const BatchParams& p, int rows_per_cta
 // Partial attention of 16 MT rows over a range of keys.  With VALUES the rows'
 // unnormalised O, maximum and sum.  Without, the maximum and sum alone, and
 // the prefix's scores themselves (base 2, -inf where masked) to p.scores: each
-// from operands of two bf16 halves (three products: high x high, low x high,
+// from operands of two fp16 halves (three products: high x high, low x high,
 // high x low), so that they are good to fp32.
 template <int TT, int MT, bool VALUES>
 __global__ void __launch_bounds__(kRwThreads, MT == 4 || !VALUES ? 4 : 5) qvg_attention_rows(const BatchParams p) {
@@ -224,15 +230,15 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 || !VALUES ? 4 : 5) qvg_at
       for (int t = 0; t < kTiles; ++t) {
         uint32_t b[4];
         ldm4(aK + t * 8 * kRwPitch * 2 + k4 * 64, b);
-        mma16816(s[t], q0, b[0], b[1]);
-        mma16816(s[t], q1, b[2], b[3]);
+        mma_scores(s[t], q0, b[0], b[1]);
+        mma_scores(s[t], q1, b[2], b[3]);
         if (!VALUES) {
           uint32_t w[4];
           ldm4(aK + kLow + t * 8 * kRwPitch * 2 + k4 * 64, w);
-          mma16816(s[t], u0, b[0], b[1]);
-          mma16816(s[t], u1, b[2], b[3]);
-          mma16816(s[t], q0, w[0], w[1]);
-          mma16816(s[t], q1, w[2], w[3]);
+          mma_scores(s[t], u0, b[0], b[1]);
+          mma_scores(s[t], u1, b[2], b[3]);
+          mma_scores(s[t], q0, w[0], w[1]);
+          mma_scores(s[t], q1, w[2], w[3]);
         }
       }
     }
@@ -318,10 +324,10 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 || !VALUES ? 4 : 5) qvg_at
         for (int t = 0; t < MT; ++t) {
           uint32_t pa[4];
           ldm4(aP + (t * 16 * kRwPPitch + k * 16) * 2, pa);
-          mma16816(o[t][0], pa, b[0][0], b[0][1]);
-          mma16816(o[t][1], pa, b[0][2], b[0][3]);
-          mma16816(o[t][2], pa, b[1][0], b[1][1]);
-          mma16816(o[t][3], pa, b[1][2], b[1][3]);
+          mma_values(o[t][0], pa, b[0][0], b[0][1]);
+          mma_values(o[t][1], pa, b[0][2], b[0][3]);
+          mma_values(o[t][2], pa, b[1][0], b[1][1]);
+          mma_values(o[t][3], pa, b[1][2], b[1][3]);
         }
       }
     } else {

@@ -9,8 +9,9 @@
 //   * one thread streams K and V tiles (32 KB bulk copies) through a ring of
 //     five slots, K0 V0 K1 V1 ...;
 //   * one thread issues the products, S_g = Q_g K'^T and O_g += P_g V for the
-//     two row tiles g = 0, 1 in turn (kind::f16, M = N = K = 128, fp32
-//     accumulators in tensor memory; P read from tensor memory).  P_g lies over
+//     two row tiles g = 0, 1 in turn (kind::f16, M = N = K = 128, fp16 operands
+//     for S and bf16 for O, fp32 accumulators in tensor memory; P read from
+//     tensor memory).  P_g lies over
 //     S_g's columns: the products run in the order they are issued, so S_g of
 //     the next tile follows O_g of this one without a wait;
 //   * eight warps per row tile run its softmax, two threads to a row with 64 of
@@ -162,7 +163,7 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
       auto scores = [&](int g, uint32_t slot) {
         const uint64_t a0 = rows0 + g * kTile, b0 = keys0 + slot * kTile;
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma(tS + 128 * g, a0 + desc_step(kk), b0 + desc_step(kk), kk > 0 ? 1u : 0u);
+        for (int kk = 0; kk < 8; ++kk) mma_as(tS + 128 * g, a0 + desc_step(kk), b0 + desc_step(kk), kIdescScores, kk > 0 ? 1u : 0u);
       };
       wait(&sh->q_full, 0);
       wait(&sh->full[0], 0);

@@ -6,7 +6,7 @@
 // kernel that rebuilt the tiles on the fly, as qvg_attention does, took 2.58 ms
 // for 1,520 rows over 38,000 tokens of 32 heads.  So a tile is rebuilt once,
 // into the workspace, as the 32 KB image that a bulk copy brings into shared
-// memory as it is: 128 keys x 128 channels in bf16, two halves of 64 channels,
+// memory as it is: 128 keys x 128 channels (K in fp16, V in bf16), two halves of 64 channels,
 // a key's 128 bytes of a half swizzled by key mod 8 (attention_tc.cuh).  K is
 // the K-major operand of S = Q K'^T in this layout and V the N-major one of
 // O = P V.  The rows are rotated once, too.

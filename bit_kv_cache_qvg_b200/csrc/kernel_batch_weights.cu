@@ -10,7 +10,7 @@
 // in one order, without atomics.
 //
 // A score must be good to fp32 (a sum of weights is an fp32 result), so each
-// operand is two bf16 halves and a score three products, high x high, low x
+// operand is two fp16 halves and a score three products, high x high, low x
 // high and high x low: 24 tensor instructions a pair of tiles; the products are
 // the bound.
 // Stream tiles come as a high and a low half of 32 KB through a ring of three
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
         const uint64_t a0 = own0 + (2 * g + low) * kTile, b0 = ring0 + slot * kTile;
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma(columns + 256 * g, a0 + desc_step(kk), b0 + desc_step(kk), add || kk > 0 ? 1u : 0u);
+          mma_as(columns + 256 * g, a0 + desc_step(kk), b0 + desc_step(kk), kIdescScores, add || kk > 0 ? 1u : 0u);
       };
       wait(&sh->resident, 0);
       uint32_t hi = 0, lo = 1, hi_turn = 0, lo_turn = 0;     // slots of the two halves, and which pass over the ring

@@ -384,8 +384,9 @@ typedef struct {
  *   workspace, ws_bytes  DEVICE scratch for the partial results of the ranges
  *      that the keys are cut into, 16-byte aligned, not shared with calls
  *      that may run at the same time (two captured graphs among them)
- * The products have bf16 operands (rotated queries and keys and the softmax
- * weights are rounded to bf16) and fp32 sums.
+ * Rotated queries and keys are rounded to fp16 for their products (magnitudes
+ * beyond 65504 saturate) and the softmax weights to bf16, unless a head has one
+ * or two rows, where all is fp32; sums are fp32.
  * Errors: INVALID_ARG (also Nk < 1, Nq < 1, B < 1, group < 1, Nt < 0, or
  * tables that do not cover Nk - 1 when k_pos is NULL), UNSUPPORTED (d != 128,
  * B * group * Nq, H * B or Nt of 2^23 or more, B * group * Nq * H of 2^31 or
@@ -401,9 +402,10 @@ QVG_API qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* 
  * batch, added to what it received before:
  *   out[h][j] = received[h][j] + sum over the rows of head h of softmax(...)_j
  * with the softmax of qvg_attention_batch (over the prefix and the row's own
- * tail).  Each product is taken from operands of 16 mantissa bits (the high
- * and low bf16 halves of rotated queries and keys) and every sum in fp32, in
- * an order that does not depend on the launch, so equal calls give equal bits.
+ * tail).  Products are taken from operands of 22 mantissa bits (the high and
+ * low fp16 halves of rotated queries and keys; magnitudes beyond 65504
+ * saturate) and every sum in fp32, in an order that does not depend on the
+ * launch, so equal calls give equal bits.
  *   received  DEVICE [H][Nk] fp32, or NULL: zeros
  *   out       DEVICE [H][Nk] fp32; may be `received` itself
  * Only `k` of the cache is read.  Workspace and errors as qvg_attention_batch. */

@@ -1,21 +1,24 @@
 """qvg_attention_batch, qvg_attention_weights and qvg_evict against plain
 implementations in 64 bits, at the sizes and masks where they can go wrong.
 
-Tolerances, from the kernels' arithmetic, with u = 2^-8 (half a bf16 step):
+Tolerances, from the kernels' arithmetic, with u = 2^-8 (half a bf16 step) and
+v = 2^-11 (half an fp16 step; below 2^-14 the rounding is at most 2^-25):
 
-* attention_batch: rotated queries and keys rounded to bf16, so a score is off
-  by at most eps_j = (2u + u^2 + 2^-16) sum_c |q'_c k'_jc| / sqrt(d), where
-  2^-16 covers the fp32 rotations and sums (128 terms, 2^-24 each); a weight
-  rounded to bf16 (u) and a base-2 exponential (2^-21).  A normalised weight
-  then changes by a factor between 1/F and F, F = (1 + u + 2^-21) / (1 - u -
-  2^-21) e^(2 eps), eps the row's largest, so that element c of O is off by at
-  most (F - 1) sum_j w_j |v_jc|, plus the output's rounding u |O_c| and the
-  fp32 sums over the keys (2^-24 a key).
-* attention_weights: operands of two bf16 halves leave u^2 of each operand and
-  drop the product of the low halves (u^2): eps_j = (3 u^2 + 2^-16) sum |..| /
-  sqrt(d) of that kind, F = e^(2 eps) (1 + 2^-20) with the scores' and the
-  logarithm's fp32 rounding, 2^-23 (|s| + |lse|), in the exponent; each row adds
-  (F - 1) w, and the sums over rows and onto `received` 2^-24 a term."""
+* attention_batch: rotated queries and keys rounded to fp16, so a score is off
+  by at most eps_j = (2v + v^2 + 2^-16) sum_c |q'_c k'_jc| / sqrt(d) + 2^-25
+  sum_c (|q'_c| + |k'_jc|) / sqrt(d), where 2^-16 covers the fp32 rotations and
+  sums (128 terms, 2^-24 each); a weight rounded to bf16 (u) and a base-2
+  exponential (2^-21).  A normalised weight then changes by a factor between
+  1/F and F, F = (1 + u + 2^-21) / (1 - u - 2^-21) e^(2 eps), eps the row's
+  largest, so that element c of O is off by at most (F - 1) sum_j w_j |v_jc|,
+  plus the output's rounding u |O_c| and the fp32 sums over the keys (2^-24 a
+  key).
+* attention_weights: operands of two fp16 halves leave v^2 of each operand (or
+  2^-25) and drop the product of the low halves (v^2): eps_j = (3 v^2 + 2^-16)
+  sum |q' k'| / sqrt(d) + 2^-25 sum (|q'| + |k'|) / sqrt(d), F = e^(2 eps)
+  (1 + 2^-20) with the scores' and the logarithm's fp32 rounding, 2^-23 (|s| +
+  |lse|), in the exponent; each row adds (F - 1) w, and the sums over rows and
+  onto `received` 2^-24 a term."""
 import numpy as np
 import pytest
 import torch
@@ -24,7 +27,7 @@ from gpu_util import np_bits, values
 
 pytestmark = pytest.mark.gpu
 D = 128
-U = 2.0 ** -8
+U, V = 2.0 ** -8, 2.0 ** -11
 
 
 @pytest.fixture(scope="module")
@@ -100,7 +103,7 @@ class Case:
                     k_pos=None if self.k_pos is None else self.k_pos.cuda(), causal=self.causal)
 
     def rows(self):
-        """(b, j, h, scores, sum |q' k'| / sqrt(d), mask, values) of the Nq rows of each sequence and query head."""
+        """(b, j, h, scores, sum |q' k'| / sqrt(d), 2^-25 sum (|q'| + |k'|) / sqrt(d), mask, values) of the Nq rows of each sequence and query head."""
         for b in range(self.B):
             n = self.lens[b] if self.Nt else 0
             pos = self.q_pos[b].numpy()
@@ -117,7 +120,8 @@ class Case:
                     sees = sees & (at[None] <= pos[:, None])
                 for j in range(h * self.group, (h + 1) * self.group):
                     qr = rotated(values(np_bits(self.Q[b, j])), np.maximum(pos, 0))
-                    yield b, j, h, qr @ k.T / np.sqrt(D), np.abs(qr) @ np.abs(k).T / np.sqrt(D), sees, v
+                    small = 2.0 ** -25 * (np.abs(qr).sum(1)[:, None] + np.abs(k).sum(1)[None]) / np.sqrt(D)
+                    yield b, j, h, qr @ k.T / np.sqrt(D), np.abs(qr) @ np.abs(k).T / np.sqrt(D), small, sees, v
 
 
 def softmax(s, sees):
@@ -133,10 +137,10 @@ def softmax(s, sees):
 def check_attention(case, O):
     O = values(np_bits(O))
     assert np.isfinite(O).all()
-    for b, j, h, s, mag, sees, v in case.rows():
+    for b, j, h, s, mag, small, sees, v in case.rows():
         w, _ = softmax(s, sees)
         ref = w @ v
-        eps = (2 * U + U * U + 2.0 ** -16) * np.where(sees, mag, 0.0).max(1)
+        eps = np.where(sees, (2 * V + V * V + 2.0 ** -16) * mag + small, 0.0).max(1)
         F = (1 + U + 2.0 ** -21) / (1 - U - 2.0 ** -21) * np.exp(2 * eps)
         bound = (F - 1 + s.shape[1] * 2.0 ** -24)[:, None] * (w @ np.abs(v))
         bound = bound + U * (np.abs(ref) + bound) + 1e-30
@@ -151,9 +155,9 @@ def check_weights(case, out, received=None):
     ref = np.zeros((H, Nk)) if received is None else received.cpu().numpy().astype(np.float64).copy()
     bound = np.abs(ref) * 2.0 ** -23 + 1e-30
     rows = case.B * case.group * case.Nq
-    for b, j, h, s, mag, sees, v in case.rows():
+    for b, j, h, s, mag, small, sees, v in case.rows():
         w, lse = softmax(s, sees)
-        eps = (3 * U * U + 2.0 ** -16) * np.where(sees, mag, 0.0).max(1)
+        eps = np.where(sees, (3 * V * V + 2.0 ** -16) * mag + small, 0.0).max(1)
         eps = eps + 2.0 ** -23 * (np.abs(np.where(sees, s, 0.0)).max(1) + np.where(np.isfinite(lse), np.abs(lse), 0.0))
         F = np.exp(2 * eps) * (1 + 2.0 ** -20 + s.shape[1] * 2.0 ** -24)
         ref[h] += w[:, :Nk].sum(0)

@@ -15,8 +15,7 @@
 //     S_g's columns: the products run in the order they are issued, so S_g of
 //     the next tile follows O_g of this one without a wait;
 //   * eight warps per row tile run its softmax, two threads to a row with 64 of
-//     its scores in registers each; they exchange their maxima through shared
-//     memory.  While one tile's softmax runs, the other's products do.  The
+//     its scores in registers each.  While one tile's softmax runs, the other's products do.  The
 //     reference maximum rises only when a row's maximum exceeds it by more than
 //     8 (base 2), so O is rescaled rarely.
 // Every wait is bounded and gives up when another role has; the kernel then
@@ -43,8 +42,11 @@ struct __align__(8) AdShared {
   uint64_t drained;               // after a failed wait: every product issued is complete
   uint32_t tmem_base;
   int abort_flag;
-  __nv_bfloat16 top[2][2][kAtTile];   // the maxima of a row's two halves
+  float top[2][2][kAtTile];       // the maxima of a row's two halves, scaled
 };
+
+constexpr int kAdSharedBytes = 3 * 1024;
+static_assert(sizeof(AdShared) <= kAdSharedBytes, "the barriers' part of shared memory");
 
 // B operand of O += P V: V's image holds a key's 64 channels of a half in 128
 // bytes, so B is N-major: 64 channels to the swizzled row, the other half
@@ -94,10 +96,15 @@ __device__ __forceinline__ AdPlace ad_place(const BatchParams& p) {
 
 __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sQ = smem;
+  // the barriers first, then the tiles, to the last byte there is: the start has
+  // to be a 1,024-byte boundary
+  AdShared* sh = reinterpret_cast<AdShared*>(smem_raw);
+  uint8_t* sQ = smem_raw + kAdSharedBytes;
   uint8_t* ring = sQ + 2 * kAtOpBytes;
-  AdShared* sh = reinterpret_cast<AdShared*>(ring + kAdSlots * kAtOpBytes);
+  if ((smem_addr(smem_raw) & 1023u) != 0) {
+    if (threadIdx.x == 0) atomicOr(p.status, 1u);
+    return;
+  }
   volatile int* abort_flag = &sh->abort_flag;
   const AdPlace a = ad_place(p);
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -247,60 +254,64 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
       ok = bar_wait_or_abort(&sh->s_done[g], (uint32_t)(j & 1), abort_flag);
       ok = !__any_sync(0xffffffffu, !ok);
       fence_after();
-      uint32_t s[2][32];
+      // The weights are taken against the reference at once; only if some row's
+      // maximum turns out more than 8 above it, it rises and they are taken again.
+      uint32_t w[2][16];
+      float2 sum[2];
+      bool gone = false;
+      for (;;) {
+        uint32_t s[2][32];
 #pragma unroll
-      for (int c = 0; c < 2; ++c) tld32_start(tSt + 32 * c, s[c]);
-      tld_wait();
+        for (int c = 0; c < 2; ++c) tld32_start(tSt + 32 * c, s[c]);
+        tld_wait();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) hold32(s[c]);
-      if (masked) {
+        for (int c = 0; c < 2; ++c) hold32(s[c]);
+        if (masked) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (__shfl_sync(0xffffffffu, kp[c], e) > limit) s[c][e] = 0xFF800000u;       // -inf
+        }
+        const float2 sl2 = make_float2(p.sl, p.sl), nm2 = make_float2(-m_run, -m_run);
+        float mx[2] = {__uint_as_float(s[0][0]), __uint_as_float(s[1][0])};
+        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int c = 0; c < 2; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (__shfl_sync(0xffffffffu, kp[c], e) > limit) s[c][e] = 0xFF800000u;       // -inf
-      }
-      float mx[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        mx[c] = __uint_as_float(s[c >> 1][16 * (c & 1)]);
-#pragma unroll
-        for (int e = 1; e < 16; ++e) mx[c] = fmaxf(mx[c], __uint_as_float(s[c >> 1][16 * (c & 1) + e]));
-      }
-      // any common reference near the maximum serves: bf16 is near enough
-      const __nv_bfloat16 mine = __float2bfloat16_rn(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-      sh->top[g][side][qi] = mine;
-      // all of S_g is in registers too: P_g may overwrite it
-      if (named_bar_or(1 + g, 256, !ok)) { ok = false; break; }
-      const float mt = fmaxf(__bfloat162float(mine), __bfloat162float(sh->top[g][side ^ 1][qi])) * p.sl;
-      const float m_new = mt > m_run + 8.0f ? mt : m_run;
-      const float alpha = exp2_approx(m_run - m_new);
-      const float2 sl2 = make_float2(p.sl, p.sl), nm2 = make_float2(-m_new, -m_new);
-      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = __ffma2_rn(make_float2(__uint_as_float(s[c][2 * e]), __uint_as_float(s[c][2 * e + 1])), sl2, nm2);
-          w[e] = pack_bf16(exp2_approx(x.x), exp2_approx(x.y));
-          // the sum of the rounded weights, the ones the product uses
-          sum[e & 1] = __fadd2_rn(sum[e & 1], make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u)));
-        }
-        tst16(tPt + 16 * c, w);
-      }
-      l_run = l_run * alpha + ((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y));
-      m_run = m_new;
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {           // rescale O_g
+          for (int e = 0; e < 16; ++e) {
+            const float u = __uint_as_float(s[c][2 * e]), v = __uint_as_float(s[c][2 * e + 1]);
+            mx[c] = fmaxf(mx[c], fmaxf(u, v));
+            const float2 x = __ffma2_rn(make_float2(u, v), sl2, nm2);
+            w[c][e] = pack_bf16(exp2_approx(x.x), exp2_approx(x.y));
+            // the sum of the rounded weights, the ones the product uses
+            sum[c] = __fadd2_rn(sum[c], make_float2(__uint_as_float(w[c][e] << 16), __uint_as_float(w[c][e] & 0xFFFF0000u)));
+          }
+        const float mine = fmaxf(mx[0], mx[1]) * p.sl;
+        sh->top[g][side][qi] = mine;
+        // (all of S_g has been read, too: P_g may overwrite it)
+        if (!named_bar_or(1 + g, 256, !ok || mine > m_run + 8.0f)) break;
+        const float m_new = fmaxf(m_run, fmaxf(mine, sh->top[g][side ^ 1][qi]));
+        gone = named_bar_or(1 + g, 256, !ok);
+        if (gone) break;
+        const float alpha = exp2_approx(m_run - m_new);
+        l_run *= alpha;
+        m_run = m_new;
+        if (j > 0 && __any_sync(0xffffffffu, alpha != 1.0f)) {           // rescale O_g
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t rg[16];
-          tld16(tOt + 16 * c, rg);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t rg[16];
+            tld16(tOt + 16 * c, rg);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) rg[e] = __float_as_uint(__uint_as_float(rg[e]) * alpha);
-          tst16(tOt + 16 * c, rg);
+            for (int e = 0; e < 16; ++e) rg[e] = __float_as_uint(__uint_as_float(rg[e]) * alpha);
+            tst16(tOt + 16 * c, rg);
+          }
         }
       }
+      if (gone) { ok = false; break; }
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tst16(tPt + 16 * c, w[c]);
+      l_run += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       fence_before();
       warp_arrive(&sh->p_full[g], lane);
@@ -359,7 +370,7 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
   }
 }
 
-size_t ad_smem_bytes() { return 1024 + (size_t)(2 + kAdSlots) * kAtOpBytes + sizeof(AdShared); }
+size_t ad_smem_bytes() { return kAdSharedBytes + (size_t)(2 + kAdSlots) * kAtOpBytes; }
 
 }  // namespace
 

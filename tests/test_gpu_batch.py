@@ -180,6 +180,12 @@ SHAPES = [
     dict(H=1, Nk=900, Nq=520, T=1, G=32, mode=1, K=256),
     dict(H=1, Nk=400, Nq=3, T=5, K=32, B=2, Nt=9),                                # the stage count at run time
     dict(H=1, Nk=515, Nq=290, T=6, K=32, group=2, causal=True, gaps=True),
+    dict(Nk=260, B=2, Nt=3, lens=[0, 3], G=8, K=256, mode=1),                     # two rows, the smallest groups
+    dict(Nk=131, B=3, Nt=70, lens=[70, 64, 1], T=8, G=128),                       # three rows, eight stages
+    dict(H=1, Nk=200, Nq=64, Nt=1, T=2),                                          # the most rows without the tensor-core kernels' tiles
+    dict(H=1, Nk=129, Nq=65, Nt=129, T=0, G=32, causal=True),                     # one more
+    dict(H=2, Nk=256, Nq=129, B=3, Nt=200, lens=[0, 200, 128], T=1),              # an empty tail among long ones
+    dict(H=1, Nk=100, Nq=20, B=4, group=2, Nt=40, lens=[40, 0, 7, 39], causal=True, G=8),   # many rows, few to a sequence
 ]
 
 
@@ -360,6 +366,77 @@ def test_evict_orders_every_kind_of_weight(q, seed):
         check_evict(q, kp, vp, w.cuda(), keep, first, recent)
     check_evict(q, kp, vp, torch.full((2, N), 2.5).cuda(), 100, 10, 10)
     check_evict(q, kp, vp, torch.full((2, N), float("nan")).cuda(), 100, 10, 10)
+
+
+def test_evict_of_many_heads(q):
+    """So many heads that a head has one CTA, and more tokens than its shared
+    memory holds weights of."""
+    g = torch.Generator().manual_seed(1)
+    H, N = 80, 49_200
+    cfg = q.config(K=16, T=1, group_size=128, scale_mode=1)
+    kp = streams(q, g, cfg, H, N)
+    w = torch.rand((H, N), generator=g)
+    w[:, ::3] = 0.25
+    check_evict(q, kp, kp, w.cuda(), 30_001, 100, 200)
+
+
+def test_evict_on_another_stream_and_captured(q):
+    g = torch.Generator().manual_seed(2)
+    cfg = q.config(K=16, T=2, group_size=64)
+    kp, vp = streams(q, g, cfg, 2, 9000), streams(q, g, cfg, 2, 9000)
+    w = [torch.rand((2, 9000), generator=g).cuda() for _ in range(2)]
+    want = [q.evict(kp, vp, x, 5000, first=3, recent=70) for x in w]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    e = q.evict(kp, vp, w[0], 5000, first=3, recent=70, stream=side)
+    side.synchronize()
+    assert torch.equal(e.kept, want[0].kept) and torch.equal(e.v.codes, want[0].v.codes)
+    now = w[0].clone()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        e = q.evict(kp, vp, now, 5000, first=3, recent=70)
+    for x, r in zip(w, want):
+        now.copy_(x)
+        gr.replay()
+        torch.cuda.synchronize()
+        for a, b in ((e.kept, r.kept), (e.pos, r.pos), (e.weights, r.weights), (e.k.codes, r.k.codes), (e.k.assign, r.k.assign),
+                     (e.v.scale, r.v.scale), (e.v.zero, r.v.zero)):
+            assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(q):
+    """The last head of a cache of more than 4 GiB of codes gives the bits that
+    it gives alone."""
+    H, N = 18, 8_000_000
+    cfg = q.config(K=16, T=1, group_size=128, scale_mode=1)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    big = q.alloc_packed(cfg, N, H)
+    assert big.codes.numel() > 1 << 32
+    big.codes.random_(0, 256, generator=g)
+    big.scale.fill_(0x28)                               # 2^-2
+    big.assign.random_(0, 16, generator=g)
+    big.centroids.normal_(generator=g)
+    one = q.Packed(codes=big.codes[-1:], scale=big.scale[-1:], zero=big.zero, assign=big.assign[:, -1:],
+                   centroids=big.centroids[:, -1:], cfg=cfg, N=N, H=1, d=D, dtype=q.BF16)
+    tables = q.rope_tables(N + 200)
+    for Nq in (1, 16, 80):
+        Q = torch.randn((1, H, Nq, D), generator=g, device="cuda").to(torch.bfloat16)
+        pos = (N + torch.arange(Nq, device="cuda")).reshape(1, -1)
+        O = q.attention_batch(big, big, Q, pos, tables)
+        alone = q.attention_batch(one, one, Q[:, -1:].contiguous(), pos, tables)
+        # cut into other ranges: the weights round against other references
+        assert (O[0, -1].float() - alone[0, 0].float()).abs().max() <= 2.0 ** -6 * alone.float().abs().max()
+        W = q.attention_weights(big, Q, pos, tables)
+        alone = q.attention_weights(one, Q[:, -1:].contiguous(), pos, tables)
+        assert (W[-1] - alone[0]).abs().max() <= 1e-5 * alone.max()
+        del O, alone
+    w = torch.rand((H, N), generator=g, device="cuda")
+    e = q.evict(big, big, w, 1_000_000)
+    a = q.evict(one, one, w[-1:].contiguous(), 1_000_000)
+    assert torch.equal(e.kept[-1], a.kept[0]) and torch.equal(e.k.codes[-1], a.k.codes[0]) and torch.equal(e.k.assign[:, -1], a.k.assign[:, 0])
+    assert torch.equal(e.weights[-1], a.weights[0])
+    assert q.workspace_status(tables) == 0
 
 
 def test_attend_accumulate_evict_together(q, ora):

@@ -14,7 +14,7 @@
 // taken against a reference that the warps share and that rises only when a
 // row's maximum exceeds it by more than 8 (base 2).  With few rows the
 // rebuilding is the bound, and with it the latency of the centroid rows and
-// the rotary table: small CTAs, five to an SM, overlap one's products with
+// the rotary table: small CTAs, four to an SM, overlap one's products with
 // another's loads.
 #include <algorithm>
 
@@ -86,7 +86,7 @@ __device__ __forceinline__ Place place_of(const BatchParams& p, int rows_per_cta
 // from operands of two fp16 halves (three products: high x high, low x high,
 // high x low), so that they are good to fp32.
 template <int TT, int MT, bool VALUES>
-__global__ void __launch_bounds__(kRwThreads, MT == 4 || !VALUES ? 4 : 5) qvg_attention_rows(const BatchParams p) {
+__global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_rows(const BatchParams p) {
   constexpr int kRows = 16 * MT;
   constexpr int kWarpKeys = 16 * MT;              // of a step's 64
   constexpr int kTiles = kWarpKeys / 8;           // tiles of 8 keys of a warp
@@ -425,51 +425,80 @@ __global__ void __launch_bounds__(128) qvg_weights_rows(const BatchParams p, con
 }
 
 // The ranges of every row joined: O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s
-// with M = max_s m_s, rounded to bf16; zeros for a row that sees nothing.  W
-// warps to a row, each with every W-th range, a lane per four channels.
-template <int W>
-__global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p) {
-  __shared__ float4 acc_s[4][32];
-  __shared__ float2 ml_s[4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, part = warp % W;
-  const int64_t row = (int64_t)blockIdx.x * (4 / W) + warp / W, stride = p.R * p.H;
-  float M = kNoMax, L = 0.0f;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  if (row < stride) {
-#pragma unroll 4
-    for (int s = part; s < p.slots; s += W) {
-      const float2 ml = __ldg(p.part_ml + s * stride + row);
-      if (ml.y == 0.0f) continue;                  // an empty range
-      const float4 x = __ldg(reinterpret_cast<const float4*>(p.part_O + (s * stride + row) * kD) + lane);
-      const float mn = fmaxf(M, ml.x), f = ex2(M - mn), w = ex2(ml.x - mn);
-      acc.x = acc.x * f + w * x.x; acc.y = acc.y * f + w * x.y; acc.z = acc.z * f + w * x.z; acc.w = acc.w * f + w * x.w;
-      L = L * f + w * ml.y;
-      M = mn;
-    }
-  }
-  if (W > 1) {
-    acc_s[warp][lane] = acc;
-    if (lane == 0) ml_s[warp] = make_float2(M, L);
-    __syncthreads();
-    if (part != 0) return;
-    float top = kNoMax;
-#pragma unroll
-    for (int w = 0; w < W; ++w) top = fmaxf(top, ml_s[warp + w].x);
-    L = 0.0f;
-    acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float f = ex2(ml_s[warp + w].x - top);
-      const float4 x = acc_s[warp + w][lane];
-      acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
-      L += f * ml_s[warp + w].y;
-    }
-  }
-  if (row >= stride) return;
+// with M = max_s m_s, rounded to bf16; zeros for a row that sees nothing.  A
+// lane per four channels.
+__device__ __forceinline__ void store_joined(const BatchParams& p, int64_t row, const float4& acc, float L) {
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
   const int h = (int)(row / p.R);
-  reinterpret_cast<uint2*>(p.O + query_row(p, h, row - (int64_t)h * p.R) * kD)[lane] =
+  reinterpret_cast<uint2*>(p.O + query_row(p, h, row - (int64_t)h * p.R) * kD)[threadIdx.x & 31] =
       make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
+}
+
+// Few ranges: a warp per row, with a running maximum.
+__global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), stride = p.R * p.H;
+  if (row >= stride) return;
+  float M = kNoMax, L = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = 0; s < p.slots; ++s) {
+    const float2 ml = __ldg(p.part_ml + s * stride + row);
+    if (ml.y == 0.0f) continue;                    // an empty range
+    const float4 x = __ldg(reinterpret_cast<const float4*>(p.part_O + (s * stride + row) * kD) + lane);
+    const float mn = fmaxf(M, ml.x), f = ex2(M - mn), w = ex2(ml.x - mn);
+    acc.x = acc.x * f + w * x.x; acc.y = acc.y * f + w * x.y; acc.z = acc.z * f + w * x.z; acc.w = acc.w * f + w * x.w;
+    L = L * f + w * ml.y;
+    M = mn;
+  }
+  store_joined(p, row, acc, L);
+}
+
+// Many: four warps per row.  The factors first, a lane to a range, then every
+// warp adds up every fourth range: with a running maximum the loads waited for
+// one another (16 us for 64 ranges of 256 rows, now 11).
+__global__ void __launch_bounds__(128) qvg_batch_merge_wide(const BatchParams p) {
+  __shared__ float4 acc_s[4][32];
+  __shared__ float factor[128];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = blockIdx.x, stride = p.R * p.H;
+  float2 ml[4];
+  float M = kNoMax, L = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int s = 32 * i + lane;
+    ml[i] = s < p.slots ? __ldg(p.part_ml + s * stride + row) : make_float2(kNoMax, 0.0f);
+    M = fmaxf(M, ml[i].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float f = ml[i].y == 0.0f ? 0.0f : ex2(ml[i].x - M);         // an empty range has no O
+    L += f * ml[i].y;
+    if (warp == 0) factor[32 * i + lane] = f;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  __syncthreads();
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const float4* src = reinterpret_cast<const float4*>(p.part_O + row * kD) + lane;
+#pragma unroll 8
+  for (int s = warp; s < p.slots; s += 4) {
+    const float f = factor[s];
+    if (f == 0.0f) continue;
+    const float4 x = __ldg(src + s * stride * (kD / 4));
+    acc.x += f * x.x; acc.y += f * x.y; acc.z += f * x.z; acc.w += f * x.w;
+  }
+  acc_s[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) {
+    const float4 x = acc_s[w][lane];
+    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+  }
+  store_joined(p, row, acc, L);
 }
 
 size_t rows_smem(int T, int G, int mt, bool values) {
@@ -511,12 +540,12 @@ cudaError_t launch_rows(const BatchParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs to an SM: five (or four) by their registers, fewer where the rows or
+// CTAs to an SM: four (three) by their registers, fewer where the rows or
 // small groups need more shared memory.
 int rows_per_sm(const BatchParams& p, bool values) {
   const size_t smem = rows_smem(p.T, p.G, p.row_tiles, values) + 1024;
   const int n = (int)(size_t(228 * 1024) / smem);
-  return std::min(n, values && p.row_tiles < 4 ? 5 : 4);
+  return std::min(n, p.row_tiles == 4 ? 3 : 4);
 }
 
 cudaError_t launch_rows_partial(const BatchParams& p, bool values, cudaStream_t s) {
@@ -530,8 +559,8 @@ cudaError_t launch_rows_weights(const BatchParams& p, const float* received, flo
 
 cudaError_t launch_batch_merge(const BatchParams& p, cudaStream_t s) {
   const int64_t rows = p.R * p.H;
-  if (p.slots > 8) qvg_batch_merge<4><<<(unsigned)rows, 128, 0, s>>>(p);
-  else qvg_batch_merge<1><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p);
+  if (p.slots > 8) qvg_batch_merge_wide<<<(unsigned)rows, 128, 0, s>>>(p);
+  else qvg_batch_merge<<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 

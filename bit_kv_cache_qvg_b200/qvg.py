@@ -522,18 +522,24 @@ class Evicted:
     weights: torch.Tensor     # [H][keep] fp32
 
 
-def _closed(p: Packed, keep: int) -> Packed:
-    """Streams for `keep` tokens a head beside p's own centroid tables."""
-    ng, H, T = p.d // p.cfg.group_size, p.H, p.cfg.T
-    # one allocation, each stream from a 256-byte boundary
-    shapes = [(H, keep, p.d // 4), (H, keep, ng), (H, keep, ng) if p.cfg.scale_mode == ASYM else (0, keep, ng), (T, H, keep)]
-    at = [0]
-    for a, b, c in shapes:
-        at.append(at[-1] + (a * b * c + 255) // 256 * 256)
-    buf = p.codes.new_empty(at[-1])
-    codes, scale, zero, assign = (buf.as_strided(s, (s[1] * s[2], s[2], 1), o) for s, o in zip(shapes, at))
-    return Packed(codes=codes, scale=scale, zero=zero if p.cfg.scale_mode == ASYM else p.zero, assign=assign,
-                  centroids=p.centroids, cfg=p.cfg, N=keep, H=H, d=p.d, dtype=p.dtype)
+def _closed(kp: Packed, vp: Packed, keep: int):
+    """Streams for `keep` tokens a head beside kp's and vp's own centroid tables,
+    in one allocation, each stream from a 256-byte boundary."""
+    H, d, T = kp.H, kp.d, kp.cfg.T
+    w, ng = d // 4, d // kp.cfg.group_size
+    n = H * keep
+    codes, groups, assign = (n * w + 255) & -256, (n * ng + 255) & -256, (n * T + 255) & -256
+    asym = kp.cfg.scale_mode == ASYM
+    size = codes + groups * (2 if asym else 1) + assign
+    cut = kp.codes.new_empty(2 * size).as_strided
+    by_code, by_group, by_token = (keep * w, w, 1), (keep * ng, ng, 1), (n, keep, 1)
+    out = []
+    for p, at in ((kp, 0), (vp, size)):
+        scale = at + codes
+        out.append(Packed(cut((H, keep, w), by_code, at), cut((H, keep, ng), by_group, scale),
+                          cut((H, keep, ng), by_group, scale + groups) if asym else p.zero,
+                          cut((T, H, keep), by_token, at + size - assign), p.centroids, p.cfg, keep, H, d, p.dtype))
+    return out
 
 
 def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int = 0, recent: int = 0,
@@ -548,10 +554,10 @@ def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int =
     at_w = _device_tensor(weights, "weights", torch.float32, shape, dev)
     at_pos = _device_tensor(k_pos, "k_pos", torch.int64, shape, dev)
     _on_device(kp.codes, vp.codes)
-    e = Evicted(k=_closed(kp, keep), v=_closed(vp, keep),
-                kept=torch.empty((kp.H, keep), dtype=torch.int32, device=dev),
-                pos=torch.empty((kp.H, keep), dtype=torch.int64, device=dev),
-                weights=weights.new_empty((kp.H, keep)))
+    k, v = _closed(kp, vp, keep)
+    shape = (kp.H, keep)
+    e = Evicted(k, v, torch.empty(shape, dtype=torch.int32, device=dev), torch.empty(shape, dtype=torch.int64, device=dev),
+                weights.new_empty(shape))
     if stream is not None:
         _lent(stream, e.kept, e.pos, e.weights, *(t for p in (e.k, e.v) for t in (p.codes, p.scale, p.zero, p.assign)))
     _check(_queue(dev, stream, lib().qvg_evict, C.byref(kp.cfg), C.byref(kp.struct()), C.byref(vp.struct()), kp.N, kp.H, kp.d, at_w,

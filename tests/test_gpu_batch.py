@@ -339,7 +339,7 @@ def check_evict(q, kp, vp, w, keep, first, recent, k_pos=None):
     (1, 1, 1, 0, 0, 1, 64, 0), (2, 2, 1, 0, 1, 0, 32, 0), (1, 3, 3, 1, 1, 2, 64, 0), (2, 37, 20, 4, 16, 1, 8, 0),
     (3, 500, 376, 4, 32, 2, 16, 1), (2, 1025, 1, 0, 0, 4, 128, 0), (1, 4097, 4000, 7, 100, 8, 128, 1),
     (2, 10240, 5000, 0, 0, 1, 64, 0),           # the shared memory of a head's weights just above 40 KB
-    (2, 12289, 5001, 3, 9, 3, 32, 0), (1, 49152, 30000, 11, 13, 1, 64, 1), (2, 60001, 777, 5, 10, 2, 64, 0),
+    (2, 12289, 5001, 3, 9, 3, 32, 0), (1, 49152, 30000, 11, 13, 1, 64, 1), (2, 60001, 777, 5, 10, 2, 64, 0), (2, 300, 123, 5, 10, 0, 32, 0),
 ])
 def test_evict_matches_the_definition(q, H, N, keep, first, recent, T, G, mode):
     g = torch.Generator().manual_seed(N + keep)

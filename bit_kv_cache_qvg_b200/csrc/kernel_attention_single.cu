@@ -1,6 +1,5 @@
-// kernel_attention_single.cu -- the kernel of qvg_attention_batch and
-// qvg_attention_weights for one or two rows a head: a token of one sequence,
-// or of two that share a prefix.
+// kernel_attention_single.cu -- the kernel of qvg_attention_batch for one row a
+// head, a token of one sequence, and of qvg_attention_weights for one or two.
 //
 // With so few rows a tensor-core tile would be mostly padding, and the way there
 // (keys rounded to bf16, stored, read back as operands) costs more than the
@@ -297,8 +296,8 @@ int single_per_sm(const BatchParams& p, bool values) {
 }
 
 cudaError_t launch_single_partial(const BatchParams& p, bool values, cudaStream_t s) {
-  if (p.R > 1) return values ? launch_single_r<2, true>(p, s) : launch_single_r<2, false>(p, s);
-  return values ? launch_single_r<1, true>(p, s) : launch_single_r<1, false>(p, s);
+  if (values) return launch_single_r<1, true>(p, s);
+  return p.R > 1 ? launch_single_r<2, false>(p, s) : launch_single_r<1, false>(p, s);
 }
 
 }  // namespace qvg

@@ -386,9 +386,14 @@ cudaError_t launch_batch_attend(const BatchParams& p, cudaStream_t s) {
 namespace {
 
 constexpr int kRowStep = 64;                      // keys of a step of the kernels for few rows
-constexpr int kSingleStep = 32;                   // and of one or two rows
-constexpr int64_t kSingleRows = 2;
-constexpr int64_t kManyRows = 64;                 // rows beyond which tcgen05 takes over
+constexpr int kSingleStep = 32;                   // and of one or two
+// Rows beyond which tcgen05 takes over, and up to which registers do.  One
+// pass over 16,000 tokens of 32 heads (K = 256, T = 2, G = 64):
+//   attention   1 row 97 us in registers; 2 rows 115, and 107 by mma.sync; 64 rows
+//               169 by mma.sync, 65 rows 163 by tcgen05;
+//   weights     2 rows 75 us in registers, 3 rows 89 by mma.sync; 64 rows 216 by
+//               mma.sync, 65 rows 244 by tcgen05.
+constexpr int64_t kManyRows = 64;
 constexpr int64_t kFewMaxRanges = 64;              // ranges of few rows
 constexpr size_t kImageBudget = size_t(1) << 30;  // operand tiles in the workspace at a time, about
 
@@ -433,7 +438,7 @@ struct BatchPlan {
   bool tc1, tc2;                  // prefix, tails
   int S1, S2, Hn;                 // ranges; heads at a time
   int row_tiles;
-  bool single;                    // one or two rows: kernel_attention_single.cu
+  bool single;                    // one row (weights: or two): kernel_attention_single.cu
   size_t bytes;
 };
 
@@ -486,7 +491,7 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
   const int64_t few = plan.tc1 ? p.RB : p.R;       // rows of the CTAs of the kernels for few rows
   plan.row_tiles = few <= 16 ? 1 : few <= 32 ? 2 : 4;
   p.row_tiles = plan.row_tiles;
-  plan.single = p.R <= kSingleRows;
+  plan.single = p.R <= (values ? 1 : 2);
   const int64_t tile = 16 * plan.row_tiles, step = plan.single ? kSingleStep : kRowStep;
   const int64_t room = (int64_t)sms * (plan.single ? single_per_sm(p, values) : rows_per_sm(p, values));
   const int64_t steps1 = plan.tc1 ? 0 : (p.Nk + step - 1) / step, steps2 = plan.tc2 ? 0 : (p.Nt + step - 1) / step;

@@ -385,8 +385,8 @@ typedef struct {
  *      that the keys are cut into, 16-byte aligned, not shared with calls
  *      that may run at the same time (two captured graphs among them)
  * Rotated queries and keys are rounded to fp16 for their products (magnitudes
- * beyond 65504 saturate) and the softmax weights to bf16, unless a head has one
- * or two rows, where all is fp32; sums are fp32.
+ * beyond 65504 saturate) and the softmax weights to bf16, unless a head has one row,
+ * where all is fp32; sums are fp32.
  * Errors: INVALID_ARG (also Nk < 1, Nq < 1, B < 1, group < 1, Nt < 0, or
  * tables that do not cover Nk - 1 when k_pos is NULL), UNSUPPORTED (d != 128,
  * B * group * Nq, H * B or Nt of 2^23 or more, B * group * Nq * H of 2^31 or

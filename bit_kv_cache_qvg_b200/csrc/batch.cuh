@@ -59,6 +59,7 @@ struct BatchParams {
   uint32_t* status;
 };
 
+constexpr int kMaxSlots = 256;                    // ranges of the prefix and a tail together, at most
 constexpr int64_t kImageBytes = 128 * kD * 2;     // one 128 x 128 bf16 operand tile
 
 cudaError_t launch_rows_partial(const BatchParams& p, bool values, cudaStream_t s);      // kernel_attention_rows.cu

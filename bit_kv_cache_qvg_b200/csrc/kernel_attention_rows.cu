@@ -459,13 +459,14 @@ __global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p) {
 // one another (16 us for 64 ranges of 256 rows, now 11).
 __global__ void __launch_bounds__(128) qvg_batch_merge_wide(const BatchParams p) {
   __shared__ float4 acc_s[4][32];
-  __shared__ float factor[128];
+  __shared__ float factor[kMaxSlots];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = blockIdx.x, stride = p.R * p.H;
-  float2 ml[4];
+  constexpr int kPer = kMaxSlots / 32;
+  float2 ml[kPer];
   float M = kNoMax, L = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int s = 32 * i + lane;
     ml[i] = s < p.slots ? __ldg(p.part_ml + s * stride + row) : make_float2(kNoMax, 0.0f);
     M = fmaxf(M, ml[i].x);
@@ -473,7 +474,7 @@ __global__ void __launch_bounds__(128) qvg_batch_merge_wide(const BatchParams p)
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const float f = ml[i].y == 0.0f ? 0.0f : ex2(ml[i].x - M);         // an empty range has no O
     L += f * ml[i].y;
     if (warp == 0) factor[32 * i + lane] = f;

@@ -32,7 +32,7 @@ namespace {
 constexpr int kAdThreads = 576;                   // 16 softmax warps, the issuer's, the loader's
 constexpr int kAdRows = 256;                      // rows per CTA
 constexpr int kAdSlots = 5;                       // ring of operand tiles
-constexpr int kAdMaxRanges = 16;                  // of the prefix
+constexpr int kAdMaxRanges = 64;                  // of the prefix, and of a tail
 
 struct __align__(8) AdShared {
   uint64_t full[kAdSlots], empty[kAdSlots];
@@ -386,7 +386,7 @@ cudaError_t launch_batch_attend(const BatchParams& p, cudaStream_t s) {
 namespace {
 
 constexpr int kRowStep = 64;                      // keys of a step of the kernels for few rows
-constexpr int kSingleStep = 32;                   // and of one or two
+constexpr int kSingleStep = 32;                   // and in registers
 // Rows beyond which tcgen05 takes over, and up to which registers do.  One
 // pass over 16,000 tokens of 32 heads (K = 256, T = 2, G = 64):
 //   attention   1 row 97 us in registers; 2 rows 115, and 107 by mma.sync; 64 rows
@@ -394,7 +394,9 @@ constexpr int kSingleStep = 32;                   // and of one or two
 //   weights     2 rows 75 us in registers, 3 rows 89 by mma.sync; 64 rows 216 by
 //               mma.sync, 65 rows 244 by tcgen05.
 constexpr int64_t kManyRows = 64;
-constexpr int64_t kFewMaxRanges = 64;              // ranges of few rows
+constexpr int64_t kFewMaxRanges = 128;             // ranges of few rows, of the prefix and of a tail
+static_assert(2 * kFewMaxRanges <= kMaxSlots && 2 * kAdMaxRanges <= kMaxSlots && kAdMaxRanges + kFewMaxRanges <= kMaxSlots,
+              "slots of partial results");
 constexpr size_t kImageBudget = size_t(1) << 30;  // operand tiles in the workspace at a time, about
 
 BatchParams params_of(const BatchArgs& a) {
@@ -513,8 +515,9 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
     const int64_t u1 = (p.Rp / kAdRows) * plan.Hn, u2 = plan.tc2 ? (p.RBp / kAdRows) * plan.Hn * p.B : 0;
     double best = -1.0;
     for (int64_t s1 = 1; s1 <= std::min<int64_t>(p.nt1, kAdMaxRanges); ++s1) {
+      if (s1 > 16 && (double)(u1 * s1) > 2.0 * sms) break;            // beyond two waves more ranges gain nothing
       const double t1 = (double)((p.nt1 + s1 - 1) / s1) + 3.0;
-      const int64_t s2 = u2 > 0 ? std::max<int64_t>(1, std::min<int64_t>(p.nt2, (int64_t)((double)p.nt2 / t1 + 0.5))) : 0;
+      const int64_t s2 = u2 > 0 ? std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(p.nt2, kAdMaxRanges), (int64_t)((double)p.nt2 / t1 + 0.5))) : 0;
       const double t2 = s2 > 0 ? (double)((p.nt2 + s2 - 1) / s2) + 3.0 : 0.0;
       const double waves = std::ceil((double)(u1 * s1) / sms);
       double cost = waves * t1;

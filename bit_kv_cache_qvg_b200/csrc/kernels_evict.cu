@@ -236,8 +236,9 @@ __device__ __forceinline__ void store_row(uint8_t* dst, const uint4& v, int n) {
 // is on its way before it writes: stores between the loads made a chain of a
 // dozen memory latencies of it.
 __global__ void __launch_bounds__(2 * kEvTile) qvg_evict_gather(const EvictParams p) {
-  const int h = blockIdx.y, side = threadIdx.x & 1;
-  const int64_t i = (int64_t)blockIdx.x * kEvTile + (threadIdx.x >> 1);
+  const unsigned tiles = (unsigned)((p.keep + kEvTile - 1) / kEvTile);
+  const int h = (int)(blockIdx.x / tiles), side = threadIdx.x & 1;
+  const int64_t i = (int64_t)(blockIdx.x % tiles) * kEvTile + (threadIdx.x >> 1);
   if (i >= p.keep) return;
   const int64_t out = (int64_t)h * p.keep + i;
   const int32_t f = __ldg(p.kept + out);
@@ -307,8 +308,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   cfg.numAttrs = p.cluster > 1 ? 1 : 0;
   if ((e = cudaLaunchKernelEx(&cfg, qvg_evict_select, p)) != cudaSuccess) return e;
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const dim3 grid((unsigned)((a.keep + kEvTile - 1) / kEvTile), (unsigned)a.H);
-  qvg_evict_gather<<<grid, 2 * kEvTile, 0, s>>>(p);
+  qvg_evict_gather<<<(unsigned)((a.keep + kEvTile - 1) / kEvTile * a.H), 2 * kEvTile, 0, s>>>(p);
   return cudaGetLastError();
 }
 

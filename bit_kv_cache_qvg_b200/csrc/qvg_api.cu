@@ -722,7 +722,8 @@ qvg_status qvg_evict(const qvg_config* cfg, const qvg_packed* k, const qvg_packe
       if (in->codes == out->codes || in->scale == out->scale || (cfg->T > 0 && in->assign == out->assign) ||
           (cfg->scale_mode == QVG_SCALE_ASYM && in->zero == out->zero))
         return QVG_ERR_INVALID_ARG;
-  if (k_out->codes == v_out->codes || weights_out == weights || (pos_out != nullptr && pos_out == k_pos))
+  if (k_out->codes == v_out->codes || k_out->scale == v_out->scale || (cfg->T > 0 && k_out->assign == v_out->assign) ||
+      (cfg->scale_mode == QVG_SCALE_ASYM && k_out->zero == v_out->zero) || weights_out == weights || (pos_out != nullptr && pos_out == k_pos))
     return QVG_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   EvictArgs a{};

@@ -125,6 +125,10 @@ def test_evict_refuses_outputs_that_are_inputs(q):
         out[field] = at
         assert evict(q, ko=packed(q, **out)) == 1, field
         assert evict(q, vo=packed(q, **{**out, "codes": out["codes"] + (0 if field == "codes" else 0x5000)})) == 1, field
+    for field, at in (("codes", 0x102000), ("scale", 0x103000), ("zero", 0x104000), ("assign", 0x105000)):
+        out = dict(codes=0x107000, scale=0x108000, zero=0x109000, assign=0x10A000)
+        out[field] = at                       # both caches' outputs in one place
+        assert evict(q, vo=packed(q, **out)) == 1, field
     for bad in (dict(codes=None), dict(codes=0x2008), dict(scale=0x3004), dict(zero=None), dict(assign=None)):
         assert evict(q, k=packed(q, **bad)) == 1, bad
 

@@ -248,6 +248,20 @@ def test_large_scores_and_far_positions(q, ora, Nq):
     check_weights(case, q.attention_weights(case.kp, **case.args()))
 
 
+@pytest.mark.parametrize("kw", [
+    dict(H=1, Nk=20000),                                                          # as many ranges as one head is cut into
+    dict(H=1, Nk=9000, Nq=3, Nt=9000, causal=True),                               # of the prefix and of the tail
+    dict(H=1, Nk=20000, Nq=70),
+    dict(H=1, Nk=20, Nq=65, Nt=66000),                                            # a tail much longer than the prefix
+    dict(H=1, Nk=9000, Nq=10, B=7, Nt=9000, lens=[9000, 0, 1, 4500, 64, 65, 8999]),
+], ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items() if k != "lens"))
+def test_few_heads_are_cut_into_many_ranges(q, ora, kw):
+    case = Case(q, ora, seed=len(str(kw)), **kw)
+    check_attention(case, q.attention_batch(case.kp, case.vp, **case.args()))
+    check_weights(case, q.attention_weights(case.kp, **case.args()))
+    assert q.workspace_status(case.tables) == 0
+
+
 def test_every_sequence_alone_gives_the_same(q, ora):
     """A batch of sequences gives each row what it gets alone, within the
     rounding of the weights against other running maxima."""
@@ -378,6 +392,18 @@ def test_evict_of_many_heads(q):
     w = torch.rand((H, N), generator=g)
     w[:, ::3] = 0.25
     check_evict(q, kp, kp, w.cuda(), 30_001, 100, 200)
+
+
+def test_evict_of_more_heads_than_a_grid_is_high(q):
+    g = torch.Generator().manual_seed(4)
+    H, N = 70_000, 5
+    kp = streams(q, g, q.config(K=16, T=0, group_size=128, scale_mode=1), H, N)
+    w = torch.argsort(torch.rand((H, N), generator=g), dim=1).float().cuda()      # a permutation of 0 .. 4 each
+    e = q.evict(kp, kp, w, 2, first=1)
+    best = w[:, 1:].argmax(1) + 1
+    assert torch.equal(e.kept.long(), torch.stack([torch.zeros_like(best), best], 1))
+    assert torch.equal(e.k.codes, torch.gather(kp.codes, 1, e.kept.long()[:, :, None].expand(-1, -1, D // 4)))
+    assert torch.equal(e.v.scale, torch.gather(kp.scale, 1, e.kept.long()[:, :, None]))
 
 
 def test_evict_on_another_stream_and_captured(q):

@@ -11,8 +11,12 @@
 // the K-major operand of S = Q K'^T in this layout and V the N-major one of
 // O = P V.  The rows are rotated once, too.
 //
-// The floor is the 512 bytes written a token; what bounds it is the
-// arithmetic of the rebuilding (rebuild.cuh).
+// The floor is the 512 bytes written a token: 95 us for 32 heads of 38,000
+// tokens.  It takes 220 us (K = 256, T = 2, G = 64; 47 us for 12 heads of
+// 14,040): the rebuilding (rebuild.cuh) keeps the issue slots, the ALU and the L1
+// data path each a half busy, and the latency of the centroid rows does the
+// rest.  So small CTAs, six to an SM: with one of 1,024 threads that keeps
+// one head's tables in the SM's L1 and loads a step ahead it took 289 us.
 #include "attention_tc.cuh"
 #include "batch.cuh"
 #include "rebuild.cuh"
@@ -96,7 +100,7 @@ __device__ __forceinline__ void expand_tile(const BatchParams& p, uint8_t* smem,
   };
   if (!tail) {
     const Rebuild<TT, kAtTile> rebuild(p, w, h, c);
-#pragma unroll 2
+#pragma unroll 1
     for (int pass = 0; pass < kExPasses; ++pass) {
       uint4 x[2];
       rebuild(nlut, tokens, pass * kExKeys + key0, x);
@@ -105,7 +109,7 @@ __device__ __forceinline__ void expand_tile(const BatchParams& p, uint8_t* smem,
   } else {
     // a tail's tokens are bf16 rows already; behind its length zeros
     const __nv_bfloat16* rows = p.tail[w] + ((int64_t)b * p.H + h) * p.Nt * kD + 8 * c;
-#pragma unroll 2
+#pragma unroll 1
     for (int pass = 0; pass < kExPasses; ++pass) {
       const int key = tile0 + pass * kExKeys + key0;
       uint4 x[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
@@ -123,7 +127,7 @@ __device__ __forceinline__ void expand_tile(const BatchParams& p, uint8_t* smem,
 // tails', the rows by head, the rows by sequence.  PRECISE: the second image
 // of a tile holds the keys' low halves instead of the values.
 template <int TT, bool PRECISE>
-__global__ void __launch_bounds__(kExThreads) qvg_batch_expand(const BatchParams p, const int64_t tiles_p, const int64_t tiles_t,
+__global__ void __launch_bounds__(kExThreads, TT >= 0 && TT <= 2 ? 6 : 4) qvg_batch_expand(const BatchParams p, const int64_t tiles_p, const int64_t tiles_t,
                                                               const int64_t row_tiles) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kKinds = PRECISE ? 1 : 2;

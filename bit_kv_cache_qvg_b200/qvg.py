@@ -436,7 +436,7 @@ def _workspace(workspace, size_call, p: Packed, b: _Batch, dev, stream) -> torch
         else:
             with torch.cuda.device(dev):
                 need = size_call(C.byref(p.cfg), p.N, p.H, C.byref(b))
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = p.codes.new_empty(need)
         _lent(stream, workspace)
     elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
         raise QvgError(1, f"the workspace must be a contiguous uint8 tensor on {dev}")
@@ -556,8 +556,8 @@ def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int =
     _on_device(kp.codes, vp.codes)
     k, v = _closed(kp, vp, keep)
     shape = (kp.H, keep)
-    e = Evicted(k, v, torch.empty(shape, dtype=torch.int32, device=dev), torch.empty(shape, dtype=torch.int64, device=dev),
-                weights.new_empty(shape))
+    new = weights.new_empty
+    e = Evicted(k, v, new(shape, dtype=torch.int32), new(shape, dtype=torch.int64), new(shape))
     if stream is not None:
         _lent(stream, e.kept, e.pos, e.weights, *(t for p in (e.k, e.v) for t in (p.codes, p.scale, p.zero, p.assign)))
     _check(_queue(dev, stream, lib().qvg_evict, C.byref(kp.cfg), C.byref(kp.struct()), C.byref(vp.struct()), kp.N, kp.H, kp.d, at_w,

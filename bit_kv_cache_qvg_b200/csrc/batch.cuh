@@ -87,13 +87,15 @@ __device__ __forceinline__ int clamp_pos(int64_t pos) {
 __device__ __forceinline__ int64_t rope_row(const BatchParams& p, int64_t pos) {
   return pos < 0 ? 0 : pos > p.max_pos ? p.max_pos : pos;
 }
+// Rows are below 2^23: 32-bit divisions (a 64-bit one takes about a hundred
+// instructions).
 __device__ __forceinline__ int64_t query_row(const BatchParams& p, int h, int64_t r) {
-  const int64_t b = r / p.RB;
-  return (b * p.H + h) * p.RB + (r - b * p.RB);
+  const uint32_t b = (uint32_t)r / (uint32_t)p.RB;
+  return ((int64_t)b * p.H + h) * p.RB + ((uint32_t)r - b * (uint32_t)p.RB);
 }
 __device__ __forceinline__ int64_t query_pos(const BatchParams& p, int64_t r) {
-  const int64_t b = r / p.RB;
-  return __ldg(p.q_pos + b * p.Nq + (r - b * p.RB) % p.Nq);
+  const uint32_t b = (uint32_t)r / (uint32_t)p.RB;
+  return __ldg(p.q_pos + b * p.Nq + ((uint32_t)r - b * (uint32_t)p.RB) % (uint32_t)p.Nq);
 }
 __device__ __forceinline__ int row_limit(const BatchParams& p, int64_t pos) {
   return pos < 0 ? kLimitNone : p.causal ? clamp_pos(pos) : kLimitAll;

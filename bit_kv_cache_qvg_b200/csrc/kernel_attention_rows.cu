@@ -110,8 +110,9 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
   const int mt = warp % MT, kg = warp / MT;       // the warp's rows and keys
   fill_nlut(p, nlut);
   // the rows, rotated
-  for (int e = threadIdx.x; e < kRows * 16; e += kRwThreads) {
-    const int r = e >> 4, cb = e & 15;
+#pragma unroll (MT < 4 ? 2 * MT : 4)
+  for (int i = 0; i < kRows * 16 / kRwThreads; ++i) {
+    const int r = (int)(threadIdx.x >> 4) + i * (kRwThreads / 16), cb = threadIdx.x & 15;
     uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
     if (a.r0 + r < a.r1) {
       const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.Q + query_row(p, a.h, a.r0 + r) * kD + 8 * cb));
@@ -389,30 +390,42 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
 __global__ void __launch_bounds__(128) qvg_weights_rows(const BatchParams p, const float* received, float* out) {
   extern __shared__ float lse[];
   const int per = (int)((p.Nk + 511) / 512), hl = (int)(blockIdx.x / per), h = p.h0 + hl;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t stride = (int64_t)p.H * p.R;
-  for (int64_t r = warp; r < p.R; r += 4) {
+  // as many lanes to a row (a power of two) as let all rows go at once, or two
+  int per_row = 32;
+  while (per_row > 2 && per_row * p.R > 128) per_row >>= 1;
+  for (int r0 = 0; r0 < (int)p.R; r0 += 128 / per_row) {
+    const int r = r0 + (int)threadIdx.x / per_row;
     float M = kNoMax, L = 0.0f;
-    for (int s = lane; s < p.slots; s += 32) {
-      const float2 ml = __ldg(p.part_ml + s * stride + (int64_t)h * p.R + r);
-      const float mn = fmaxf(M, ml.x);
-      L = L * ex2(M - mn) + ml.y * ex2(ml.x - mn);
+    const float2* ml = p.part_ml + (int64_t)h * p.R + min(r, (int)p.R - 1);
+#pragma unroll 1
+    for (int s0 = (int)threadIdx.x % per_row; s0 < p.slots; s0 += 8 * per_row) {
+      float2 x[8];
+      float mn = M, sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int s = s0 + i * per_row;
+        x[i] = s < p.slots ? __ldg(ml + s * stride) : make_float2(kNoMax, 0.0f);
+        mn = fmaxf(mn, x[i].x);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += x[i].y * ex2(x[i].x - mn);
+      L = L * ex2(M - mn) + sum;
       M = mn;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
+    for (int o = per_row >> 1; o > 0; o >>= 1) {
       const float m2 = __shfl_xor_sync(0xffffffffu, M, o), l2 = __shfl_xor_sync(0xffffffffu, L, o), mn = fmaxf(M, m2);
       L = L * ex2(M - mn) + l2 * ex2(m2 - mn);
       M = mn;
     }
-    if (lane == 0) lse[r] = L == 0.0f ? INFINITY : M + log2f(L);
+    if (r < (int)p.R && threadIdx.x % per_row == 0) lse[r] = L == 0.0f ? INFINITY : M + log2f(L);
   }
   __syncthreads();
   const int64_t j = (int64_t)(blockIdx.x % per) * 512 + 4 * threadIdx.x;
   if (j >= p.Nk) return;
   const float* x = p.scores + (int64_t)hl * p.R * p.Nkp + j;
   float4 sum = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
+#pragma unroll 8
   for (int64_t r = 0; r < p.R; ++r) {
     const float4 v = __ldg(reinterpret_cast<const float4*>(x + r * p.Nkp));
     const float z = lse[r];

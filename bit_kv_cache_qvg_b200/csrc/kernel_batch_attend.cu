@@ -79,20 +79,18 @@ __device__ __forceinline__ AdPlace ad_place(const BatchParams& p) {
   AdPlace a;
   const int64_t first_tail = (int64_t)p.S1 * p.tiles1 * p.Hn;
   a.tail = blockIdx.x >= first_tail;
-  const int64_t e = a.tail ? blockIdx.x - first_tail : blockIdx.x;
-  const int S = a.tail ? p.S2 : p.S1;
-  const int64_t nb = a.tail ? p.tiles2 : p.tiles1;
-  const int range = (int)(e % S);
-  const int64_t block = e / S % nb, unit = e / S / nb;
-  a.hl = (int)(unit % p.Hn);
+  const uint32_t e = (uint32_t)(a.tail ? blockIdx.x - first_tail : blockIdx.x);
+  const uint32_t S = (uint32_t)(a.tail ? p.S2 : p.S1), nb = (uint32_t)(a.tail ? p.tiles2 : p.tiles1);
+  const uint32_t range = e % S, block = e / S % nb, unit = e / S / nb;
+  a.hl = (int)(unit % (uint32_t)p.Hn);
   a.h = p.h0 + a.hl;
-  a.b = (int)(unit / p.Hn);
+  a.b = (int)(unit / (uint32_t)p.Hn);
   a.n = (int)(a.tail ? tail_length(p, a.b) : p.Nk);
-  a.slot = a.tail ? p.slot2 + range : range;
+  a.slot = (int)(a.tail ? p.slot2 + range : range);
   a.r0 = (int)((a.tail ? a.b * p.RB : 0) + block * kAdRows);
   a.r1 = (int)(a.tail ? (a.b + 1) * p.RB : p.R);
   a.groups = a.r1 - a.r0 > kAtTile ? 2 : 1;
-  const int64_t nt = (a.n + kAtTile - 1) / kAtTile;
+  const uint32_t nt = (uint32_t)(a.n + kAtTile - 1) / kAtTile;       // below 2^16, S at most 64
   a.j0 = (int)(nt * range / S);
   a.ntiles = (int)(nt * (range + 1) / S) - a.j0;
   return a;
@@ -398,6 +396,11 @@ constexpr int kSingleStep = 32;                   // and in registers
 //   weights     2 rows 75 us in registers, 3 rows 89 by mma.sync; 64 rows 216 by
 //               mma.sync, 65 rows 244 by tcgen05.
 constexpr int64_t kManyRows = 64;
+// Attention of more rows stays with mma.sync while it is so little that the
+// launches count: blocks of 64 rows x 64 keys in all.  256 rows: 2 heads of 2,000
+// tokens (256 blocks) 25.5 us by mma.sync, 32.5 by tcgen05; 12 of 512 (384) 27.6
+// and 32.5; 2 of 5,000 (632) 34.1 and 34.6; 12 of 2,000 (1,536) 50.3 and 36.7.
+constexpr int64_t kFewBlocks = 400;
 constexpr int64_t kFewMaxRanges = 128;             // ranges of few rows, of the prefix and of a tail
 static_assert(2 * kFewMaxRanges <= kMaxSlots && 2 * kAdMaxRanges <= kMaxSlots && kAdMaxRanges + kFewMaxRanges <= kMaxSlots,
               "slots of partial results");
@@ -491,7 +494,8 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
 BatchPlan plan_batch(BatchParams& p, bool values) {
   BatchPlan plan{};
   const double sms = (double)device_sm_count();
-  plan.tc1 = p.R > kManyRows;
+  const int64_t blocks = ((p.R + 63) / 64 * ((p.Nk + 63) / 64) + p.B * ((p.RB + 63) / 64) * ((p.Nt + 63) / 64)) * p.H;
+  plan.tc1 = p.R > kManyRows && !(values && blocks <= kFewBlocks);
   plan.tc2 = plan.tc1 && p.Nt > 0 && p.RB > kManyRows;
   plan.Hn = p.H;
   const int64_t few = plan.tc1 ? p.RB : p.R;       // rows of the CTAs of the kernels for few rows

@@ -35,9 +35,10 @@ __device__ __forceinline__ void expand_rows(const BatchParams& p, bool by_sequen
   const int which = by_sequence ? 1 : 0;
   const int64_t rows = by_sequence ? p.RB : p.R, pad = by_sequence ? p.RBp : p.Rp;
   const int64_t base = ((by_sequence ? (int64_t)b * p.Hn : 0) + hl) * 2 * pad;
-  for (int e = threadIdx.x; e < 128 * 16; e += kExThreads) {
-    const int cb = e & 15;
-    const int64_t r = tile * 128 + (e >> 4);
+  const int cb = threadIdx.x & 15;
+#pragma unroll 2
+  for (int i = 0; i < 128 * 16 / kExThreads; ++i) {
+    const int64_t r = tile * 128 + (threadIdx.x >> 4) + i * (kExThreads / 16);
     uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
     if (r < rows) {
       const int64_t row = by_sequence ? b * p.RB + r : r;
@@ -127,18 +128,17 @@ __device__ __forceinline__ void expand_tile(const BatchParams& p, uint8_t* smem,
 // tails', the rows by head, the rows by sequence.  PRECISE: the second image
 // of a tile holds the keys' low halves instead of the values.
 template <int TT, bool PRECISE>
-__global__ void __launch_bounds__(kExThreads, TT >= 0 && TT <= 2 ? 6 : 4) qvg_batch_expand(const BatchParams p, const int64_t tiles_p, const int64_t tiles_t,
-                                                              const int64_t row_tiles) {
+__global__ void __launch_bounds__(kExThreads, TT >= 0 && TT <= 2 ? 6 : 4) qvg_batch_expand(const BatchParams p, const uint32_t tiles_p, const uint32_t tiles_t,
+                                                              const uint32_t row_tiles) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kKinds = PRECISE ? 1 : 2;
-  int64_t id = blockIdx.x;
+  uint32_t id = blockIdx.x;
   if (id >= kKinds * (tiles_p + tiles_t)) {
     id -= kKinds * (tiles_p + tiles_t);
     const bool by_sequence = id >= row_tiles;
     if (by_sequence) id -= row_tiles;
-    const int64_t per = (by_sequence ? p.RBp : p.Rp) / 128;
-    const int64_t unit = id / per;
-    expand_rows<PRECISE>(p, by_sequence, (int)(unit % p.Hn), (int)(unit / p.Hn), id % per);
+    const uint32_t per = (uint32_t)(by_sequence ? p.RBp : p.Rp) / 128, unit = id / per;
+    expand_rows<PRECISE>(p, by_sequence, (int)(unit % (uint32_t)p.Hn), (int)(unit / (uint32_t)p.Hn), id % per);
     return;
   }
   // all K tiles first, then all V tiles: neighbouring CTAs read the same tables
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kExThreads, TT >= 0 && TT <= 2 ? 6 : 4) qvg_ba
   if (values) id -= tiles_p + tiles_t;
   const bool tail = id >= tiles_p;
   if (tail) id -= tiles_p;
-  const int64_t nt = tail ? p.nt2 : p.nt1, unit = id / nt;
-  const int j = (int)(id % nt), hl = (int)(unit % p.Hn), b = (int)(unit / p.Hn), h = p.h0 + hl;
+  const uint32_t nt = (uint32_t)(tail ? p.nt2 : p.nt1), unit = id / nt;
+  const int j = (int)(id % nt), hl = (int)(unit % (uint32_t)p.Hn), b = (int)(unit / (uint32_t)p.Hn), h = p.h0 + hl;
   const int n = (int)(tail ? tail_length(p, b) : p.Nk);
   const int tile0 = j * kAtTile;
   if (tile0 >= n) return;                          // a tail's tile that nobody reads
@@ -163,8 +163,9 @@ cudaError_t expand_t(const BatchParams& p, bool precise, cudaStream_t s) {
   const int64_t rows_h = p.S1 > 0 ? p.Hn * (p.Rp / 128) : 0, rows_s = p.S2 > 0 ? p.B * p.Hn * (p.RBp / 128) : 0;
   const unsigned grid = (unsigned)((precise ? 1 : 2) * (tiles_p + tiles_t) + rows_h + rows_s);
   const size_t smem = 16 * sizeof(float2) + kAtTile * sizeof(uint32_t) + Tokens<TT, kAtTile>::bytes(kD / p.G);
-  if (precise) qvg_batch_expand<TT, true><<<grid, kExThreads, smem, s>>>(p, tiles_p, tiles_t, rows_h);
-  else qvg_batch_expand<TT, false><<<grid, kExThreads, smem, s>>>(p, tiles_p, tiles_t, rows_h);
+  const uint32_t np = (uint32_t)tiles_p, nt = (uint32_t)tiles_t, nr = (uint32_t)rows_h;
+  if (precise) qvg_batch_expand<TT, true><<<grid, kExThreads, smem, s>>>(p, np, nt, nr);
+  else qvg_batch_expand<TT, false><<<grid, kExThreads, smem, s>>>(p, np, nt, nr);
   return cudaGetLastError();
 }
 

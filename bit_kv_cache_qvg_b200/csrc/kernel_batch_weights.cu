@@ -56,22 +56,20 @@ __device__ __forceinline__ WtPlace wt_place(const BatchParams& p) {
   if (STATS) {
     const int64_t first_tail = (int64_t)p.S1 * p.tiles1 * p.Hn;
     a.tail = blockIdx.x >= first_tail;
-    const int64_t e = a.tail ? blockIdx.x - first_tail : blockIdx.x;
-    const int S = a.tail ? p.S2 : p.S1;
-    const int64_t nb = a.tail ? p.tiles2 : p.tiles1;
-    const int range = (int)(e % S);
-    const int64_t block = e / S % nb, unit = e / S / nb;
-    a.hl = (int)(unit % p.Hn);
-    a.b = (int)(unit / p.Hn);
+    const uint32_t e = (uint32_t)(a.tail ? blockIdx.x - first_tail : blockIdx.x);
+    const uint32_t S = (uint32_t)(a.tail ? p.S2 : p.S1), nb = (uint32_t)(a.tail ? p.tiles2 : p.tiles1);
+    const uint32_t range = e % S, block = e / S % nb, unit = e / S / nb;
+    a.hl = (int)(unit % (uint32_t)p.Hn);
+    a.b = (int)(unit / (uint32_t)p.Hn);
     a.n = (int)(a.tail ? tail_length(p, a.b) : p.Nk);
-    a.slot = a.tail ? p.slot2 + range : range;
+    a.slot = (int)(a.tail ? p.slot2 + range : range);
     a.first = (int)((a.tail ? a.b * p.RB : 0) + block * 2 * kAtTile);
     a.end = (int)(a.tail ? (a.b + 1) * p.RB : p.R);
-    const int64_t nt = (a.n + kAtTile - 1) / kAtTile;
+    const uint32_t nt = (uint32_t)(a.n + kAtTile - 1) / kAtTile;     // below 2^16, S at most 64
     a.j0 = (int)(nt * range / S);
     a.steps = (int)(nt * (range + 1) / S) - a.j0;
   } else {
-    const int64_t per = (p.nt1 + 1) / 2;
+    const uint32_t per = (uint32_t)(p.nt1 + 1) / 2;
     a.tail = false;
     a.hl = (int)(blockIdx.x / per);
     a.b = 0;
@@ -352,9 +350,16 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
       named_bar_or(1 + g, 256, false);
       if (side == 0) total += half->x;
     }
+    // a single range: nothing for qvg_batch_lse to join
+    if (STATS && ok && side == 0 && p.slots == 1) {
+      const bool seen = limit != kLimitNone && total != 0.0f;
+      const int64_t at = (int64_t)a.hl * p.Rp + mine;
+      p.lse[at] = seen ? m_run + log2f(total) : INFINITY;
+      p.limits[at] = seen ? limit : kLimitAll;
+    }
     if (ok && in && side == 0) {
       if (STATS) {
-        p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + mine] = make_float2(m_run, limit == kLimitNone ? 0.0f : total);
+        if (p.slots > 1) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + mine] = make_float2(m_run, limit == kLimitNone ? 0.0f : total);
       } else {
         const int64_t at = (int64_t)a.h * p.Nk + mine;
         out[at] = (received != nullptr ? received[at] : 0.0f) + total;
@@ -411,8 +416,10 @@ cudaError_t launch_batch_stats(const BatchParams& p, cudaStream_t s) {
 cudaError_t launch_batch_weights(const BatchParams& p, float* lse, int* limits, const float* received, float* out, cudaStream_t s) {
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(qvg_batch_weights<false>), wt_smem_bytes());
   if (e != cudaSuccess) return e;
-  qvg_batch_lse<<<(unsigned)((p.Hn * p.Rp + 255) / 256), 256, 0, s>>>(p, lse, limits);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.slots > 1) {
+    qvg_batch_lse<<<(unsigned)((p.Hn * p.Rp + 255) / 256), 256, 0, s>>>(p, lse, limits);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
   qvg_batch_weights<false><<<(unsigned)((p.nt1 + 1) / 2 * p.Hn), kWtThreads, wt_smem_bytes(), s>>>(p, lse, limits, received, out);
   return cudaGetLastError();
 }

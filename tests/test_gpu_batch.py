@@ -186,6 +186,15 @@ SHAPES = [
     dict(H=1, Nk=129, Nq=65, Nt=129, T=0, G=32, causal=True),                     # one more
     dict(H=2, Nk=256, Nq=129, B=3, Nt=200, lens=[0, 200, 128], T=1),              # an empty tail among long ones
     dict(H=1, Nk=100, Nq=20, B=4, group=2, Nt=40, lens=[40, 0, 7, 39], causal=True, G=8),   # many rows, few to a sequence
+    # enough blocks of 64 rows x 64 keys for the tensor-core kernels
+    dict(H=2, Nk=2601, Nq=130, B=2, Nt=130, T=2, G=128, mode=1, gaps=True, K=64),
+    dict(H=3, Nk=1700, Nq=300, B=2, Nt=300, causal=True, T=2, K=64, lens=[300, 150]),
+    dict(H=3, Nk=2300, Nq=300, T=1, G=32, mode=1, K=256),
+    dict(H=2, Nk=2700, Nq=290, T=6, K=32, group=2, causal=True, gaps=True),
+    dict(H=3, Nk=4600, Nq=65, Nt=129, T=0, G=32, causal=True),
+    dict(H=2, Nk=2690, Nq=129, B=3, Nt=200, lens=[0, 200, 128], T=4, G=16),
+    dict(H=3, Nk=3200, Nq=20, B=4, group=2, Nt=40, lens=[40, 0, 7, 39], causal=True, T=3, G=8),
+    dict(H=2, Nk=64, Nq=1000, Nt=1000, causal=True, T=2),                         # the tail is the most of it
 ]
 
 
@@ -213,7 +222,7 @@ def test_attention_weights_match_64_bits(q, ora, kw):
     assert torch.equal(again, out)                                                # the same bits every time
 
 
-@pytest.mark.parametrize("Nq", [3, 200])
+@pytest.mark.parametrize("Nq", [3, 200, 490])                         # positions below 900: see the cache moved there
 def test_rows_that_see_nothing(q, ora, Nq):
     """Padding rows (negative positions), and causal rows before every key:
     zeros, and no weight given."""
@@ -233,7 +242,7 @@ def test_rows_that_see_nothing(q, ora, Nq):
     assert torch.count_nonzero(q.attention_weights(case.kp, **case.args())) == 0
 
 
-@pytest.mark.parametrize("Nq", [1, 300])
+@pytest.mark.parametrize("Nq", [1, 300, 1500])
 def test_large_scores_and_far_positions(q, ora, Nq):
     """Scores of several tens (a weight near 1 at one key), and a cache whose
     positions lie far out in the tables."""
@@ -274,7 +283,7 @@ def test_every_sequence_alone_gives_the_same(q, ora):
         assert (one.float() - O[b:b + 1].float()).abs().max() <= 2.0 ** -6 * O.float().abs().max()
 
 
-@pytest.mark.parametrize("Nq", [2, 300])
+@pytest.mark.parametrize("Nq", [2, 300, 700])
 def test_other_streams_and_captured_graphs(q, ora, Nq):
     """The calls on a side stream, and captured into two graphs with workspaces
     of their own that replay at the same time, give the bits of the eager call."""

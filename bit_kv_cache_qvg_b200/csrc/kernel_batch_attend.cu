@@ -485,11 +485,38 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
   return at;
 }
 
-// The cut of the keys.  For few rows: ranges of equal length, as many as run at
-// the same time (a last wave of few CTAs would double the time).  For many: the plan with the least
-// estimated time, in key tiles of a CTA that holds an SM: a CTA of t tiles
-// takes t + 3 (its start and its end), the tails' CTAs fill the gaps of the
-// prefix's last wave first, and a range's partial results cost their way
+// Estimated time, in steps (or tiles) of keys, of u1 * s1 CTAs of the prefix and
+// u2 * s2 of the tails, of which `room` run at a time: a CTA of t steps takes
+// t + start, and the tails' CTAs fill the gaps of the prefix's last wave first.
+double estimate(int64_t u1, int64_t s1, int64_t n1, int64_t u2, int64_t s2, int64_t n2, double room, double start) {
+  const double t1 = s1 > 0 ? (double)((n1 + s1 - 1) / s1) + start : 0.0, t2 = s2 > 0 ? (double)((n2 + s2 - 1) / s2) + start : 0.0;
+  const double waves = std::ceil((double)(u1 * s1) / room), free = waves * room - (double)(u1 * s1);
+  if ((double)(u2 * s2) <= free && t2 <= t1) return waves * t1;
+  const double gaps = free * t1, rest = (double)(u2 * s2) * t2 - 0.8 * gaps;
+  return waves * t1 + (rest > 0.0 ? std::max(t2, rest / room + 0.5 * t2) : 0.0);
+}
+
+// Ranges for few rows: those of the prefix fill one to four waves, with or without
+// the tails' CTAs, whose ranges are about as long; the least estimated time.
+void cut_few(int64_t u1, int64_t n1, int64_t u2, int64_t n2, int64_t room, double start, int* S1, int* S2) {
+  const bool prefix = n1 > 0;
+  const int64_t u = prefix ? u1 : u2, n = prefix ? n1 : n2;
+  double best = -1.0;
+  for (int64_t k = 1; k <= 4; ++k)
+    for (int64_t taken : {int64_t(0), prefix && n2 > 0 ? u2 : int64_t(0)}) {
+      const int64_t want = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(n, kFewMaxRanges), (k * room - taken) / u));
+      const int64_t len = (n + want - 1) / want, s = (n + len - 1) / len;
+      const int64_t s2 = prefix ? std::min<int64_t>((n2 + len - 1) / len, kFewMaxRanges) : s;
+      const double cost = estimate(u1, prefix ? s : 0, n1, u2, s2, n2, (double)room, start);
+      if (best >= 0.0 && cost >= best) continue;
+      best = cost;
+      *S1 = prefix ? (int)s : 0;
+      *S2 = (int)s2;
+    }
+}
+
+// The cut of the keys, by estimated times.  Many rows: a CTA holds an SM, its
+// start and end take 3 tiles, and a range's partial results cost their way
 // through memory (about a fifth of a tile per CTA's worth of rows and range).
 BatchPlan plan_batch(BatchParams& p, bool values) {
   BatchPlan plan{};
@@ -508,13 +535,8 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
   if (!plan.tc1 && !values)
     plan.Hn = (int)std::max<int64_t>(1, std::min<int64_t>(p.H, (int64_t)(kImageBudget / ((size_t)p.R * p.Nkp * sizeof(float)))));
   if (steps1 + steps2 > 0) {
-    // ranges of equal length, as many as run at the same time
     const int64_t units1 = (p.R + tile - 1) / tile * plan.Hn, units2 = (p.RB + tile - 1) / tile * plan.Hn * p.B;
-    const int64_t longest = std::max(steps1, steps2);
-    int64_t steps = std::max<int64_t>(1, (longest + kFewMaxRanges - 1) / kFewMaxRanges);
-    while (steps < longest && units1 * ((steps1 + steps - 1) / steps) + units2 * ((steps2 + steps - 1) / steps) > room) ++steps;
-    plan.S1 = (int)((steps1 + steps - 1) / steps);
-    plan.S2 = (int)((steps2 + steps - 1) / steps);
+    cut_few(units1, steps1, units2, steps2, room, plan.single ? 6.0 : 1.5, &plan.S1, &plan.S2);
   }
   if (plan.tc1) {
     size_t per_head = (size_t)p.nt1 * 2 * kImageBytes;
@@ -526,11 +548,7 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
       if (s1 > 16 && (double)(u1 * s1) > 2.0 * sms) break;            // beyond two waves more ranges gain nothing
       const double t1 = (double)((p.nt1 + s1 - 1) / s1) + 3.0;
       const int64_t s2 = u2 > 0 ? std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(p.nt2, kAdMaxRanges), (int64_t)((double)p.nt2 / t1 + 0.5))) : 0;
-      const double t2 = s2 > 0 ? (double)((p.nt2 + s2 - 1) / s2) + 3.0 : 0.0;
-      const double waves = std::ceil((double)(u1 * s1) / sms);
-      double cost = waves * t1;
-      const double gaps = (waves * sms - (double)(u1 * s1)) * t1, rest = (double)(u2 * s2) * t2 - 0.8 * gaps;
-      if (rest > 0.0) cost += std::max(t2, rest / sms + 0.5 * t2);
+      double cost = estimate(u1, s1, p.nt1, u2, s2, p.nt2, sms, 3.0);
       if (s1 + s2 + (plan.tc2 ? 0 : plan.S2) > 1) cost += 2.0 + 0.2 * (double)(s1 + s2) * (double)u1 / sms;
       if (best < 0.0 || cost < best) {
         best = cost;

@@ -43,6 +43,8 @@ struct BatchParams {
   float2* part_ml;                // [slots][H][R]: (row maximum, row sum) of each range, base 2
   __nv_bfloat16* O;               // where a single slot needs no merge
   int row_tiles;                  // tiles of 16 rows to a CTA of the kernels for few rows
+  int row_cuts;                   // cuts of the rows for the sums by key (weights of many rows)
+  float* part_w;                  // [row_cuts][Hn][Nkp]: their sums, when there are several
   float* scores;                  // [Hn][R][Nkp]: the prefix's scores, base 2 (weights of few rows)
   int64_t Nkp;                    // Nk padded to 64
   // Tensor-core operands of heads h0 .. h0 + Hn - 1, laid out as the kernels'

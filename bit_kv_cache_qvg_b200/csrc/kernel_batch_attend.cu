@@ -447,6 +447,7 @@ struct BatchPlan {
   bool tc1, tc2;                  // prefix, tails
   int S1, S2, Hn;                 // ranges; heads at a time
   int row_tiles;
+  int row_cuts;                   // weights of many rows: cuts of the rows of the second pass
   bool single;                    // one row (weights: or two): kernel_attention_single.cu
   size_t bytes;
 };
@@ -474,6 +475,8 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
       p.row_lo[0] = reinterpret_cast<uint8_t*>(take((size_t)plan.Hn * p.Rp * kD * 2));
       p.lse = reinterpret_cast<float*>(take((size_t)plan.Hn * p.Rp * sizeof(float)));
       p.limits = reinterpret_cast<int*>(take((size_t)plan.Hn * p.Rp * sizeof(int)));
+      p.row_cuts = plan.row_cuts;
+      if (p.row_cuts > 1) p.part_w = reinterpret_cast<float*>(take((size_t)plan.row_cuts * plan.Hn * p.Nkp * sizeof(float)));
     }
   }
   if (plan.tc2) {
@@ -555,6 +558,19 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
         plan.S1 = (int)s1;
         if (plan.tc2) plan.S2 = (int)s2;
       }
+    }
+  }
+  plan.row_cuts = 1;
+  if (plan.tc1 && !values) {
+    // The sums by key of few keys leave SMs idle: cut the rows, too, where that
+    // saves more than the joining launch takes (about 2.5 tiles' time): 2 heads
+    // of 66 keys and 2,774 rows 49 us a call in one piece, 31 in cuts.
+    const int64_t units = (p.nt1 + 1) / 2 * plan.Hn, tiles = (p.R + kAtTile - 1) / kAtTile;
+    double least = estimate(units, 1, tiles, 0, 0, 0, sms, 3.0);
+    for (int64_t s = 2; s <= std::min<int64_t>(tiles, 32) && units * s <= 2 * (int64_t)sms; ++s) {
+      const int64_t per = (tiles + s - 1) / s;
+      const double cost = std::ceil((double)(units * s) / sms) * ((double)per + 3.0) + 2.5;
+      if (cost < least) { least = cost; plan.row_cuts = (int)s; }
     }
   }
   plan.bytes = place(p, plan, values, nullptr);

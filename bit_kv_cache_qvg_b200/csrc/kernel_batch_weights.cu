@@ -40,8 +40,9 @@ struct __align__(16) WtShared {
 };
 
 // What a CTA has to do.  First pass (STATS): rows r0 .. of head h over tiles
-// j0 .. of the prefix's or a tail's keys.  Second: keys 256 tile .. over all
-// rows.
+// j0 .. of the prefix's or a tail's keys.  Second: keys 256 tile .. over the
+// tiles j0 .. of rows: all of them, or where there are few keys one of the
+// plan's cuts, whose sums qvg_batch_sums joins.
 struct WtPlace {
   bool tail;
   int hl, h, b, slot;
@@ -71,14 +72,16 @@ __device__ __forceinline__ WtPlace wt_place(const BatchParams& p) {
   } else {
     const uint32_t per = (uint32_t)(p.nt1 + 1) / 2;
     a.tail = false;
-    a.hl = (int)(blockIdx.x / per);
+    const uint32_t S = (uint32_t)p.row_cuts, cut = blockIdx.x % S, e = blockIdx.x / S;
+    a.hl = (int)(e / per);
     a.b = 0;
-    a.slot = 0;
+    a.slot = (int)cut;
     a.n = (int)p.Nk;
-    a.first = (int)(blockIdx.x % per) * 2 * kAtTile;
+    a.first = (int)(e % per) * 2 * kAtTile;
     a.end = a.n;
-    a.j0 = 0;
-    a.steps = (int)((p.R + kAtTile - 1) / kAtTile);
+    const uint32_t nt = (uint32_t)(p.R + kAtTile - 1) / kAtTile;
+    a.j0 = (int)(nt * cut / S);
+    a.steps = (int)(nt * (cut + 1) / S) - a.j0;
   }
   a.h = p.h0 + a.hl;
   a.groups = a.end - a.first > kAtTile ? 2 : 1;
@@ -146,11 +149,11 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
         expect_bytes(&sh->full[slot], (uint32_t)kAtOpBytes);
         const uint32_t dst = smem_addr(ring) + slot * kAtOpBytes;
         if (STATS) load_keys(dst, a.j0 + j, (i & 1) != 0, &sh->full[slot]);
-        else load_rows(dst, (int64_t)j * kAtTile, (i & 1) != 0, &sh->full[slot]);
+        else load_rows(dst, (int64_t)(a.j0 + j) * kAtTile, (i & 1) != 0, &sh->full[slot]);
         ++issued;
         if (!STATS && (i & 1) == 0) {
           if (j > 1 && !bar_wait_or_abort(&sh->v_free[j & 1], (uint32_t)(((j >> 1) - 1) & 1), abort_flag)) { *abort_flag = 1; break; }
-          const int64_t at = (int64_t)a.hl * p.Rp + (int64_t)j * kAtTile;
+          const int64_t at = (int64_t)a.hl * p.Rp + (int64_t)(a.j0 + j) * kAtTile;
           expect_bytes(&sh->v_full[j & 1], kAtTile * 4);
           bulk_load(smem_addr(sh->lse[j & 1]), lse + at, kAtTile * 4, &sh->v_full[j & 1]);
           ++vectors;
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
           bool under = false;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            kp[c] = __ldg(limits + (int64_t)a.hl * p.Rp + j * kAtTile + 64 * side + 32 * c + lane);
+            kp[c] = __ldg(limits + (int64_t)a.hl * p.Rp + (a.j0 + j) * kAtTile + 64 * side + 32 * c + lane);
             under |= kp[c] < bound;
           }
           masked = __any_sync(0xffffffffu, under);
@@ -360,6 +363,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
     if (ok && in && side == 0) {
       if (STATS) {
         if (p.slots > 1) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + mine] = make_float2(m_run, limit == kLimitNone ? 0.0f : total);
+      } else if (p.row_cuts > 1) {
+        p.part_w[((int64_t)a.slot * p.Hn + a.hl) * p.Nkp + mine] = total;
       } else {
         const int64_t at = (int64_t)a.h * p.Nk + mine;
         out[at] = (received != nullptr ? received[at] : 0.0f) + total;
@@ -401,6 +406,20 @@ __global__ void __launch_bounds__(256) qvg_batch_lse(const BatchParams p, float*
   limits[e] = limit;
 }
 
+// out = received + the sums of the cuts of the rows, in their order.
+__global__ void __launch_bounds__(256) qvg_batch_sums(const BatchParams p, const float* received, float* out) {
+  const uint32_t per = (uint32_t)(p.Nk + 255) / 256;
+  const int hl = (int)(blockIdx.x / per);
+  const int64_t j = (int64_t)(blockIdx.x % per) * 256 + threadIdx.x;
+  if (j >= p.Nk) return;
+  const float* part = p.part_w + (int64_t)hl * p.Nkp + j;
+  float sum = 0.0f;
+#pragma unroll 8
+  for (int s = 0; s < p.row_cuts; ++s) sum += __ldg(part + (int64_t)s * p.Hn * p.Nkp);
+  const int64_t at = (int64_t)(p.h0 + hl) * p.Nk + j;
+  out[at] = (received != nullptr ? received[at] : 0.0f) + sum;
+}
+
 size_t wt_smem_bytes() { return 1024 + (size_t)(4 + kWtSlots) * kAtOpBytes + sizeof(WtShared); }
 
 }  // namespace
@@ -420,7 +439,9 @@ cudaError_t launch_batch_weights(const BatchParams& p, float* lse, int* limits, 
     qvg_batch_lse<<<(unsigned)((p.Hn * p.Rp + 255) / 256), 256, 0, s>>>(p, lse, limits);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  qvg_batch_weights<false><<<(unsigned)((p.nt1 + 1) / 2 * p.Hn), kWtThreads, wt_smem_bytes(), s>>>(p, lse, limits, received, out);
+  qvg_batch_weights<false><<<(unsigned)((p.nt1 + 1) / 2 * p.Hn * p.row_cuts), kWtThreads, wt_smem_bytes(), s>>>(p, lse, limits, received, out);
+  if (p.row_cuts == 1 || (e = cudaGetLastError()) != cudaSuccess) return e != cudaSuccess ? e : cudaGetLastError();
+  qvg_batch_sums<<<(unsigned)((p.Nk + 255) / 256 * p.Hn), 256, 0, s>>>(p, received, out);
   return cudaGetLastError();
 }
 

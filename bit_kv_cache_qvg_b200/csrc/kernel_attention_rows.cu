@@ -6,7 +6,7 @@
 //   s_j = q.k_j / sqrt(d),  O = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m).
 // All rows of a K/V head (every sequence, every query head of the group) read
 // the same prefix: a CTA takes up to 64 of them and a range of the keys, 64 at a
-// time.  Its four warps rebuild the 64 keys and values into shared memory
+// time.  Its four warps (eight for the weights) rebuild the 64 keys and values into shared memory
 // (rebuild.cuh), then multiply: mma.sync m16n8k16, fp16 operands for the scores
 // and bf16 for O, fp32 sums.  For the scores a warp has 16 rows and as many of the
 // 64 keys as leave no warp idle; the weights go through shared memory, and for O a warp has 32
@@ -14,7 +14,7 @@
 // taken against a reference that the warps share and that rises only when a
 // row's maximum exceeds it by more than 8 (base 2).  With few rows the
 // rebuilding is the bound, and with it the latency of the centroid rows and
-// the rotary table: small CTAs, four to an SM, overlap one's products with
+// the rotary table: small CTAs, three or four to an SM, overlap one's products with
 // another's loads.  8 heads, 32 rows, 38,000 tokens (K = 256, T = 2): 83 us, the
 // L1 data path 65 % busy.
 #include <algorithm>
@@ -25,7 +25,7 @@
 namespace qvg {
 namespace {
 
-constexpr int kRwThreads = 128;                   // 4 warps
+__host__ __device__ constexpr int rw_warps(bool values) { return values ? 4 : 8; }
 constexpr int kRwKeys = 64;                       // keys per CTA and step
 constexpr int kRwPPitch = kRwKeys + 8;            // the same for the weights
 constexpr int kRwPitch = kD + 8;                  // padded row in shared memory (bf16): ldmatrix meets no bank twice
@@ -81,25 +81,33 @@ __device__ __forceinline__ Place place_of(const BatchParams& p, int rows_per_cta
   return a;
 }
 
+// CTAs to an SM that the registers are cut for: 16 warps with the sums of O, 24
+// without, where eight warps to a CTA leave a thread half as many scores.  The
+// weights of 64 rows over 16 heads of 11,011 tokens took 101 us with four and
+// take 86; attention of 32 rows over 8 heads of 38,000 took 87 and would 95.
+__host__ __device__ constexpr int rw_per_sm(int mt, bool values) { return values && mt < 4 ? 4 : 3; }
+
 // Partial attention of 16 MT rows over a range of keys.  With VALUES the rows'
 // unnormalised O, maximum and sum.  Without, the maximum and sum alone, and
 // the prefix's scores themselves (base 2, -inf where masked) to p.scores: each
 // from operands of two fp16 halves (three products: high x high, low x high,
 // high x low), so that they are good to fp32.
 template <int TT, int MT, bool VALUES>
-__global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_rows(const BatchParams p) {
+__global__ void __launch_bounds__(32 * rw_warps(VALUES), rw_per_sm(MT, VALUES)) qvg_attention_rows(const BatchParams p) {
+  constexpr int W = rw_warps(VALUES), kThreads = 32 * W;
   constexpr int kRows = 16 * MT;
-  constexpr int kWarpKeys = 16 * MT;              // of a step's 64
+  constexpr int kGroups = W / MT;                 // warps with the same rows
+  constexpr int kWarpKeys = kRwKeys / kGroups;    // of a step's 64
   constexpr int kTiles = kWarpKeys / 8;           // tiles of 8 keys of a warp
   extern __shared__ __align__(16) uint8_t smem[];
   __nv_bfloat16* sK = reinterpret_cast<__nv_bfloat16*>(smem);        // keys (high halves)
   __nv_bfloat16* sV = sK + kRwKeys * kRwPitch;                       // values, or the keys' low halves
   __nv_bfloat16* sQ = sV + kRwKeys * kRwPitch;                       // rows (high halves, then low)
   float2* nlut = reinterpret_cast<float2*>(sQ + (VALUES ? 1 : 2) * kRows * kRwPitch);
-  float2* sml = nlut + 16;                                           // [4][16]: a warp's rows: maxima, at the end sums
-  float* sref = reinterpret_cast<float*>(sml + 64);                  // [64]: 2^(old - new) of a raised reference, by row
-  int* sflag = reinterpret_cast<int*>(sref + 64);                    // [4]: a warp has a row that asks for it
-  int* spos = sflag + 4;                                            // [2][64]: positions for the masks, by step
+  float2* sml = nlut + 16;                                           // [W][16]: a warp's rows: maxima, at the end sums
+  float* sref = reinterpret_cast<float*>(sml + 16 * W);                // [64]: 2^(old - new) of a raised reference, by row
+  int* sflag = reinterpret_cast<int*>(sref + 64);                    // [W]: a warp has a row that asks for it
+  int* spos = sflag + W;                                                  // [2][64]: positions for the masks, by step
   uint32_t* turn = reinterpret_cast<uint32_t*>(spos + 2 * kRwKeys);  // rows of the rotary table
   using Block = Tokens<TT, kRwKeys>;
   Block& tk = *reinterpret_cast<Block*>(turn + kRwKeys);
@@ -111,8 +119,8 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
   fill_nlut(p, nlut);
   // the rows, rotated
 #pragma unroll (MT < 4 ? 2 * MT : 4)
-  for (int i = 0; i < kRows * 16 / kRwThreads; ++i) {
-    const int r = (int)(threadIdx.x >> 4) + i * (kRwThreads / 16), cb = threadIdx.x & 15;
+  for (int i = 0; i < kRows * 16 / kThreads; ++i) {
+    const int r = (int)(threadIdx.x >> 4) + i * (kThreads / 16), cb = threadIdx.x & 15;
     uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
     if (a.r0 + r < a.r1) {
       const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.Q + query_row(p, a.h, a.r0 + r) * kD + 8 * cb));
@@ -128,12 +136,13 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
     limit[i] = r < a.r1 ? row_limit(p, query_pos(p, r)) : kLimitNone;
   }
   float m[2] = {kNoMax, kNoMax}, l[2] = {0.0f, 0.0f};
-  float o[VALUES ? MT : 1][4][4];                 // O of all rows and channels 32 warp .. + 31
+  constexpr int kNt = 16 / W;                     // tiles of 8 channels of a warp
+  float o[VALUES ? MT : 1][kNt][4];               // O of all rows and channels 8 kNt warp ..
   if (VALUES) {
 #pragma unroll
     for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < kNt; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[t][n][e] = 0.0f;
   }
@@ -144,8 +153,8 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
   const __nv_bfloat16* tail_k = a.tail ? p.tail[0] + ((int64_t)a.b * p.H + a.h) * p.Nt * kD + 8 * rc : nullptr;
   const __nv_bfloat16* tail_v = a.tail && VALUES ? p.tail[1] + ((int64_t)a.b * p.H + a.h) * p.Nt * kD + 8 * rc : nullptr;
   // The bytes of a step's tokens, a step ahead in registers: threads 0 .. 63 have
-  // a key each, 64 .. 127 a value, and every thread a half of both's codes.
-  const int own = threadIdx.x & (kRwKeys - 1), w = threadIdx.x >> 6;
+  // a key each, 64 .. 127 a value, and the last 128 a half of both's codes.
+  const int own = threadIdx.x & (kRwKeys - 1), w = threadIdx.x >> 6, part = (int)threadIdx.x - (kThreads - 2 * kRwKeys);
   TokenBytes<TT> held;
   uint4 held_codes[2];
   int64_t held_pos = 0;
@@ -153,10 +162,12 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
     const int key = min(k0 + own, a.n - 1);
     if (w == 0) held_pos = raw_key_pos(p, a.tail, a.h, a.b, key);
     if (a.tail) return;
-    if (VALUES || w == 0) load_token<TT>(p, w, a.h, key, held);
-    const int64_t half = ((int64_t)a.h * p.Nk + min(k0 + (int)(threadIdx.x >> 1), a.n - 1)) * 2 + (threadIdx.x & 1);
-    held_codes[0] = __ldg(reinterpret_cast<const uint4*>(p.codes[0]) + half);
-    if (VALUES) held_codes[1] = __ldg(reinterpret_cast<const uint4*>(p.codes[1]) + half);
+    if (w < (VALUES ? 2 : 1)) load_token<TT>(p, w, a.h, key, held);
+    if (part >= 0) {
+      const int64_t half = ((int64_t)a.h * p.Nk + min(k0 + (part >> 1), a.n - 1)) * 2 + (part & 1);
+      held_codes[0] = __ldg(reinterpret_cast<const uint4*>(p.codes[0]) + half);
+      if (VALUES) held_codes[1] = __ldg(reinterpret_cast<const uint4*>(p.codes[1]) + half);
+    }
   };
   auto stash = [&](int k0, int parity) {
     const int key = k0 + own;
@@ -165,14 +176,16 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
       turn[own] = (uint32_t)rope_row(p, held_pos);
     }
     if (a.tail) return;
-    if (VALUES || w == 0) store_token<TT, kRwKeys>(p, w, a.h, min(key, a.n - 1), held, w == 0 ? tk : tv, own);
-    tk.codes[threadIdx.x] = held_codes[0];
-    if (VALUES) tv.codes[threadIdx.x] = held_codes[1];
+    if (w < (VALUES ? 2 : 1)) store_token<TT, kRwKeys>(p, w, a.h, min(key, a.n - 1), held, w == 0 ? tk : tv, own);
+    if (part >= 0) {
+      tk.codes[part] = held_codes[0];
+      if (VALUES) tv.codes[part] = held_codes[1];
+    }
   };
   // ldmatrix: a warp's rows of Q, 8 keys of K (four 8 x 8 tiles along the channels), 16 keys of V
   const uint32_t aQ = shared_addr(sQ + (16 * mt + (lane & 15)) * kRwPitch + 8 * (lane >> 4));
   const uint32_t aK = shared_addr(sK + (kWarpKeys * kg + (lane & 7)) * kRwPitch + 8 * (lane >> 3));
-  const uint32_t aV = shared_addr(sV + (lane & 15) * kRwPitch + 32 * warp + 8 * (lane >> 4));
+  const uint32_t aV = shared_addr(sV + (lane & 15) * kRwPitch + 8 * kNt * warp + 8 * (lane >> 4));
   const uint32_t aP = shared_addr(sP + (lane & 15) * kRwPPitch + 8 * (lane >> 4));
   constexpr uint32_t kLow = kRwKeys * kRwPitch * 2;          // from the keys' high halves to the low ones
   if (a.k0 < a.k1) fetch(a.k0);
@@ -183,8 +196,8 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
     __syncthreads();                               // and the last step's products have read sK and sV
     if (k0 + kRwKeys < a.k1) fetch(k0 + kRwKeys);
 #pragma unroll 2
-    for (int pass = 0; pass < kRwKeys / 16; ++pass) {
-      const int at = pass * 16 + rkey;
+    for (int pass = 0; pass < kRwKeys / (kThreads / 8); ++pass) {
+      const int at = pass * (kThreads / 8) + rkey;
       uint4 x[2], y[2];
       if (!a.tail) {
         keys(nlut, tk, at, x);
@@ -287,7 +300,7 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
       const bool raise = __any_sync(0xffffffffu, top[0] > m[0] + 8.0f || top[1] > m[1] + 8.0f);
       if (lane == 0) sflag[warp] = raise;
       __syncthreads();
-      const int4 flags = *reinterpret_cast<const int4*>(sflag);
+      const int4 flags = *reinterpret_cast<const int4*>(sflag);        // of the four warps
       if (flags.x | flags.y | flags.z | flags.w) {
         // the reference rises to the rows' maxima: weights again, sums and O rescaled
         if (c == 0) { sml[warp * 16 + g].x = top[0]; sml[warp * 16 + g + 8].x = top[1]; }
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
         for (int i = 0; i < 2; ++i) {
           float mn = m[i];
 #pragma unroll
-          for (int w2 = 0; w2 < 4 / MT; ++w2) mn = fmaxf(mn, sml[(mt + w2 * MT) * 16 + g + 8 * i].x);
+          for (int w2 = 0; w2 < kGroups; ++w2) mn = fmaxf(mn, sml[(mt + w2 * MT) * 16 + g + 8 * i].x);
           const float f = ex2(m[i] - mn);
           if (kg == 0 && c == 0) sref[16 * mt + g + 8 * i] = f;
           l[i] *= f;
@@ -308,7 +321,7 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
         for (int t = 0; t < MT; ++t) {
           const float f0 = sref[16 * t + g], f1 = sref[16 * t + g + 8];
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
+          for (int n = 0; n < kNt; ++n) {
             o[t][n][0] *= f0; o[t][n][1] *= f0;
             o[t][n][2] *= f1; o[t][n][3] *= f1;
           }
@@ -316,20 +329,18 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
       }
       l[0] += add[0];
       l[1] += add[1];
-      // O of all rows and the warp's 32 channels
+      // O of all rows and the warp's channels
 #pragma unroll
       for (int k = 0; k < kRwKeys / 16; ++k) {
-        uint32_t b[2][4];
-        ldm4t(aV + k * 16 * kRwPitch * 2, b[0]);
-        ldm4t(aV + k * 16 * kRwPitch * 2 + 32, b[1]);
+        uint32_t b[kNt / 2][4];
+#pragma unroll
+        for (int n = 0; n < kNt / 2; ++n) ldm4t(aV + k * 16 * kRwPitch * 2 + 32 * n, b[n]);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           uint32_t pa[4];
           ldm4(aP + (t * 16 * kRwPPitch + k * 16) * 2, pa);
-          mma_values(o[t][0], pa, b[0][0], b[0][1]);
-          mma_values(o[t][1], pa, b[0][2], b[0][3]);
-          mma_values(o[t][2], pa, b[1][0], b[1][1]);
-          mma_values(o[t][3], pa, b[1][2], b[1][3]);
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) mma_values(o[t][n], pa, b[n / 2][2 * (n & 1)], b[n / 2][2 * (n & 1) + 1]);
         }
       }
     } else {
@@ -360,9 +371,9 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
     for (int i = 0; i < 2; ++i) {
       float M = kNoMax, L = 0.0f;
 #pragma unroll
-      for (int w2 = 0; w2 < 4 / MT; ++w2) M = fmaxf(M, sml[(mt + w2 * MT) * 16 + g + 8 * i].x);
+      for (int w2 = 0; w2 < kGroups; ++w2) M = fmaxf(M, sml[(mt + w2 * MT) * 16 + g + 8 * i].x);
 #pragma unroll
-      for (int w2 = 0; w2 < 4 / MT; ++w2) {
+      for (int w2 = 0; w2 < kGroups; ++w2) {
         const float2 x = sml[(mt + w2 * MT) * 16 + g + 8 * i];
         L += x.y * ex2(x.x - M);
       }
@@ -377,9 +388,9 @@ __global__ void __launch_bounds__(kRwThreads, MT == 4 ? 3 : 4) qvg_attention_row
       for (int i = 0; i < 2; ++i) {
         const int r = a.r0 + 16 * t + g + 8 * i;
         if (r >= a.r1) continue;
-        float* row = p.part_O + (((int64_t)a.slot * p.H + a.h) * p.R + r) * kD + 32 * warp + 2 * c;
+        float* row = p.part_O + (((int64_t)a.slot * p.H + a.h) * p.R + r) * kD + 8 * kNt * warp + 2 * c;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) *reinterpret_cast<float2*>(row + 8 * n) = make_float2(o[t][n][2 * i], o[t][n][2 * i + 1]);
+        for (int n = 0; n < kNt; ++n) *reinterpret_cast<float2*>(row + 8 * n) = make_float2(o[t][n][2 * i], o[t][n][2 * i + 1]);
       }
   }
 }
@@ -519,7 +530,7 @@ __global__ void __launch_bounds__(128) qvg_batch_merge_wide(const BatchParams p)
 size_t rows_smem(int T, int G, int mt, bool values) {
   const size_t tiles = (size_t)(2 * kRwKeys + (values ? 1 : 2) * 16 * mt) * kRwPitch * 2;
   const size_t block = kRwKeys * (32 + sizeof(uint32_t) * (T >= 0 && T <= 4 ? (T > 0 ? T : 1) : kMaxT) + kD / G * sizeof(float2));
-  return tiles + (16 + 64) * sizeof(float2) + (64 + 4 + 3 * kRwKeys) * sizeof(int) + (values ? 2 : 1) * block +
+  return tiles + (16 + 16 * rw_warps(values)) * sizeof(float2) + (64 + rw_warps(values) + 3 * kRwKeys) * sizeof(int) + (values ? 2 : 1) * block +
          (values ? (size_t)16 * mt * kRwPPitch * 2 : 0);
 }
 
@@ -530,7 +541,7 @@ cudaError_t launch_rows_mt(const BatchParams& p, cudaStream_t s) {
   static_assert(Tokens<TT, kRwKeys>::bytes(1) == kRwKeys * (32 + sizeof(uint32_t) * Tokens<TT, kRwKeys>::TR + sizeof(float2)), "block size");
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(qvg_attention_rows<TT, MT, VALUES>), smem);
   if (e != cudaSuccess) return e;
-  qvg_attention_rows<TT, MT, VALUES><<<grid, kRwThreads, smem, s>>>(p);
+  qvg_attention_rows<TT, MT, VALUES><<<grid, 32 * rw_warps(VALUES), smem, s>>>(p);
   return cudaGetLastError();
 }
 template <int TT, bool VALUES>
@@ -555,12 +566,12 @@ cudaError_t launch_rows(const BatchParams& p, cudaStream_t s) {
 
 }  // namespace
 
-// CTAs to an SM: four (three) by their registers, fewer where the rows or
-// small groups need more shared memory.
+// CTAs to an SM: fewer than their registers allow where the rows or small groups
+// need more shared memory.
 int rows_per_sm(const BatchParams& p, bool values) {
   const size_t smem = rows_smem(p.T, p.G, p.row_tiles, values) + 1024;
   const int n = (int)(size_t(228 * 1024) / smem);
-  return std::min(n, p.row_tiles == 4 ? 3 : 4);
+  return std::min(n, rw_per_sm(p.row_tiles, values));
 }
 
 cudaError_t launch_rows_partial(const BatchParams& p, bool values, cudaStream_t s) {

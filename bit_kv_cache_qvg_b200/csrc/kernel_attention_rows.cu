@@ -6,17 +6,17 @@
 //   s_j = q.k_j / sqrt(d),  O = sum_j e^(s_j - m) v_j / sum_j e^(s_j - m).
 // All rows of a K/V head (every sequence, every query head of the group) read
 // the same prefix: a CTA takes up to 64 of them and a range of the keys, 64 at a
-// time.  Its four warps (eight for the weights) rebuild the 64 keys and values into shared memory
-// (rebuild.cuh), then multiply: mma.sync m16n8k16, fp16 operands for the scores
-// and bf16 for O, fp32 sums.  For the scores a warp has 16 rows and as many of the
-// 64 keys as leave no warp idle; the weights go through shared memory, and for O a warp has 32
-// channels of all rows, so that its sums take few registers.  The weights are
-// taken against a reference that the warps share and that rises only when a
-// row's maximum exceeds it by more than 8 (base 2).  With few rows the
-// rebuilding is the bound, and with it the latency of the centroid rows and
-// the rotary table: small CTAs, three or four to an SM, overlap one's products with
-// another's loads.  8 heads, 32 rows, 38,000 tokens (K = 256, T = 2): 83 us, the
-// L1 data path 65 % busy.
+// time.  Its four or eight warps rebuild the 64 keys and values into shared
+// memory (rebuild.cuh), then multiply: mma.sync m16n8k16, fp16 operands for the
+// scores and bf16 for O, fp32 sums.  For the scores a warp has 16 rows and as many
+// of the 64 keys as leave no warp idle; the weights go through shared memory, and
+// for O a warp has 32 channels of all rows, so that its sums take few registers.
+// The weights are taken against a reference that the warps share and that rises
+// only when a row's maximum exceeds it by more than 8 (base 2).  With few rows
+// the rebuilding is the bound, and with it the latency of the centroid rows and
+// the rotary table: small CTAs, three or four to an SM, overlap one's products
+// with another's loads.  8 heads, 32 rows, 38,000 tokens (K = 256, T = 2): 83 us,
+// the L1 data path 65 % busy.
 #include <algorithm>
 
 #include "batch.cuh"
@@ -25,7 +25,7 @@
 namespace qvg {
 namespace {
 
-__host__ __device__ constexpr int rw_warps(bool values) { return values ? 4 : 8; }
+__host__ __device__ constexpr int rw_warps(int mt, bool values) { return values || mt == 1 ? 4 : 8; }
 constexpr int kRwKeys = 64;                       // keys per CTA and step
 constexpr int kRwPPitch = kRwKeys + 8;            // the same for the weights
 constexpr int kRwPitch = kD + 8;                  // padded row in shared memory (bf16): ldmatrix meets no bank twice
@@ -81,11 +81,12 @@ __device__ __forceinline__ Place place_of(const BatchParams& p, int rows_per_cta
   return a;
 }
 
-// CTAs to an SM that the registers are cut for: 16 warps with the sums of O, 24
-// without, where eight warps to a CTA leave a thread half as many scores.  The
-// weights of 64 rows over 16 heads of 11,011 tokens took 101 us with four and
-// take 86; attention of 32 rows over 8 heads of 38,000 took 87 and would 95.
-__host__ __device__ constexpr int rw_per_sm(int mt, bool values) { return values && mt < 4 ? 4 : 3; }
+// CTAs to an SM that the registers are cut for: 16 warps (of 64 rows 12) with the
+// sums of O, 24 without, where eight warps to a CTA leave a thread half as many
+// scores.  The weights of 64 rows over 16 heads of 11,011 tokens took 101 us with
+// four warps and take 86; but 3 rows over 32 heads of 16,000 take 89 with four and would
+// 100, attention of 32 rows over 8 heads of 38,000 takes 85 and would 95.
+__host__ __device__ constexpr int rw_per_sm(int mt, bool values) { return rw_warps(mt, values) == 8 || mt == 4 ? 3 : 4; }
 
 // Partial attention of 16 MT rows over a range of keys.  With VALUES the rows'
 // unnormalised O, maximum and sum.  Without, the maximum and sum alone, and
@@ -93,8 +94,8 @@ __host__ __device__ constexpr int rw_per_sm(int mt, bool values) { return values
 // from operands of two fp16 halves (three products: high x high, low x high,
 // high x low), so that they are good to fp32.
 template <int TT, int MT, bool VALUES>
-__global__ void __launch_bounds__(32 * rw_warps(VALUES), rw_per_sm(MT, VALUES)) qvg_attention_rows(const BatchParams p) {
-  constexpr int W = rw_warps(VALUES), kThreads = 32 * W;
+__global__ void __launch_bounds__(32 * rw_warps(MT, VALUES), rw_per_sm(MT, VALUES)) qvg_attention_rows(const BatchParams p) {
+  constexpr int W = rw_warps(MT, VALUES), kThreads = 32 * W;
   constexpr int kRows = 16 * MT;
   constexpr int kGroups = W / MT;                 // warps with the same rows
   constexpr int kWarpKeys = kRwKeys / kGroups;    // of a step's 64
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(128) qvg_batch_merge_wide(const BatchParams p)
 size_t rows_smem(int T, int G, int mt, bool values) {
   const size_t tiles = (size_t)(2 * kRwKeys + (values ? 1 : 2) * 16 * mt) * kRwPitch * 2;
   const size_t block = kRwKeys * (32 + sizeof(uint32_t) * (T >= 0 && T <= 4 ? (T > 0 ? T : 1) : kMaxT) + kD / G * sizeof(float2));
-  return tiles + (16 + 16 * rw_warps(values)) * sizeof(float2) + (64 + rw_warps(values) + 3 * kRwKeys) * sizeof(int) + (values ? 2 : 1) * block +
+  return tiles + (16 + 16 * rw_warps(mt, values)) * sizeof(float2) + (64 + rw_warps(mt, values) + 3 * kRwKeys) * sizeof(int) + (values ? 2 : 1) * block +
          (values ? (size_t)16 * mt * kRwPPitch * 2 : 0);
 }
 
@@ -541,7 +542,7 @@ cudaError_t launch_rows_mt(const BatchParams& p, cudaStream_t s) {
   static_assert(Tokens<TT, kRwKeys>::bytes(1) == kRwKeys * (32 + sizeof(uint32_t) * Tokens<TT, kRwKeys>::TR + sizeof(float2)), "block size");
   const cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(qvg_attention_rows<TT, MT, VALUES>), smem);
   if (e != cudaSuccess) return e;
-  qvg_attention_rows<TT, MT, VALUES><<<grid, 32 * rw_warps(VALUES), smem, s>>>(p);
+  qvg_attention_rows<TT, MT, VALUES><<<grid, 32 * rw_warps(MT, VALUES), smem, s>>>(p);
   return cudaGetLastError();
 }
 template <int TT, bool VALUES>

@@ -391,10 +391,11 @@ constexpr int kRowStep = 64;                      // keys of a step of the kerne
 constexpr int kSingleStep = 32;                   // and in registers
 // Rows beyond which tcgen05 takes over, and up to which registers do.  One
 // pass over 16,000 tokens of 32 heads (K = 256, T = 2, G = 64):
-//   attention   1 row 97 us in registers; 2 rows 115, and 107 by mma.sync; 64 rows
-//               169 by mma.sync, 65 rows 163 by tcgen05;
-//   weights     2 rows 75 us in registers, 3 rows 89 by mma.sync; 64 rows 216 by
-//               mma.sync, 65 rows 244 by tcgen05.
+//   attention   1 row 95 us in registers; 2 rows 115, and 104 by mma.sync; 64 rows
+//               163 by mma.sync, 65 rows 163 by tcgen05 (where the time grows by 8 us
+//               up to 128 rows, by mma.sync it doubles);
+//   weights     2 rows 75 us in registers, 3 rows 87 by mma.sync; 64 rows 182 by
+//               mma.sync, 65 rows 235 by tcgen05, and more by mma.sync.
 constexpr int64_t kManyRows = 64;
 // Attention of more rows stays with mma.sync while it is so little that the
 // launches count: blocks of 64 rows x 64 keys in all.  256 rows: 2 heads of 2,000

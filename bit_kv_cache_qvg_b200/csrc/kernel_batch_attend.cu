@@ -500,23 +500,27 @@ double estimate(int64_t u1, int64_t s1, int64_t n1, int64_t u2, int64_t s2, int6
   return waves * t1 + (rest > 0.0 ? std::max(t2, rest / room + 0.5 * t2) : 0.0);
 }
 
-// Ranges for few rows: those of the prefix fill one to four waves, with or without
-// the tails' CTAs, whose ranges are about as long; the least estimated time.
+// Ranges for few rows, about as long in the prefix (n1 steps, u1 CTAs a range) as
+// in the tails: either part's CTAs fill one to four waves, with or without the
+// other's; the least estimated time.
 void cut_few(int64_t u1, int64_t n1, int64_t u2, int64_t n2, int64_t room, double start, int* S1, int* S2) {
-  const bool prefix = n1 > 0;
-  const int64_t u = prefix ? u1 : u2, n = prefix ? n1 : n2;
   double best = -1.0;
-  for (int64_t k = 1; k <= 4; ++k)
-    for (int64_t taken : {int64_t(0), prefix && n2 > 0 ? u2 : int64_t(0)}) {
-      const int64_t want = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(n, kFewMaxRanges), (k * room - taken) / u));
-      const int64_t len = (n + want - 1) / want, s = (n + len - 1) / len;
-      const int64_t s2 = prefix ? std::min<int64_t>((n2 + len - 1) / len, kFewMaxRanges) : s;
-      const double cost = estimate(u1, prefix ? s : 0, n1, u2, s2, n2, (double)room, start);
-      if (best >= 0.0 && cost >= best) continue;
-      best = cost;
-      *S1 = prefix ? (int)s : 0;
-      *S2 = (int)s2;
-    }
+  auto consider = [&](int64_t n, int64_t ranges) {
+    ranges = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(n, kFewMaxRanges), ranges));
+    const int64_t len = (n + ranges - 1) / ranges;
+    const int64_t s1 = std::min<int64_t>((n1 + len - 1) / len, kFewMaxRanges), s2 = std::min<int64_t>((n2 + len - 1) / len, kFewMaxRanges);
+    const double cost = estimate(u1, s1, n1, u2, s2, n2, (double)room, start);
+    if (best >= 0.0 && cost >= best) return;
+    best = cost;
+    *S1 = (int)s1;
+    *S2 = (int)s2;
+  };
+  for (int64_t k = 1; k <= 4; ++k) {
+    if (n1 > 0) consider(n1, k * room / u1);
+    if (n1 > 0 && n2 > 0) consider(n1, (k * room - u2) / u1);
+    if (n2 > 0) consider(n2, k * room / u2);
+    if (n1 > 0 && n2 > 0) consider(n2, (k * room - u1) / u2);
+  }
 }
 
 // The cut of the keys, by estimated times.  Many rows: a CTA holds an SM, its
@@ -550,14 +554,17 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
     double best = -1.0;
     for (int64_t s1 = 1; s1 <= std::min<int64_t>(p.nt1, kAdMaxRanges); ++s1) {
       if (s1 > 16 && (double)(u1 * s1) > 2.0 * sms) break;            // beyond two waves more ranges gain nothing
-      const double t1 = (double)((p.nt1 + s1 - 1) / s1) + 3.0;
-      const int64_t s2 = u2 > 0 ? std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(p.nt2, kAdMaxRanges), (int64_t)((double)p.nt2 / t1 + 0.5))) : 0;
-      double cost = estimate(u1, s1, p.nt1, u2, s2, p.nt2, sms, 3.0);
-      if (s1 + s2 + (plan.tc2 ? 0 : plan.S2) > 1) cost += 2.0 + 0.2 * (double)(s1 + s2) * (double)u1 / sms;
-      if (best < 0.0 || cost < best) {
-        best = cost;
-        plan.S1 = (int)s1;
-        if (plan.tc2) plan.S2 = (int)s2;
+      // a tail's ranges about as long as the prefix's, or the whole tail
+      const int64_t len = (p.nt1 + s1 - 1) / s1 + 3;
+      const int64_t cut = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(p.nt2, kAdMaxRanges), (p.nt2 + len / 2) / len));
+      for (int64_t s2 : {u2 > 0 ? cut : 0, u2 > 0 ? int64_t(1) : 0}) {
+        double cost = estimate(u1, s1, p.nt1, u2, s2, p.nt2, sms, 3.0);
+        if (s1 + s2 + (plan.tc2 ? 0 : plan.S2) > 1) cost += 2.0 + 0.2 * ((double)s1 * (double)u1 + (double)s2 * (double)u2) / sms;
+        if (best < 0.0 || cost < best) {
+          best = cost;
+          plan.S1 = (int)s1;
+          if (plan.tc2) plan.S2 = (int)s2;
+        }
       }
     }
   }

@@ -392,7 +392,8 @@ typedef struct {
  * B * group * Nq, H * B or Nt of 2^23 or more, B * group * Nq * H of 2^31 or
  * more), WORKSPACE_TOO_SMALL, CUDA,
  * DEVICE_TIMEOUT (recorded in the tables' status word by earlier work; looked
- * at by the calls whose own kernels wait, those of more than 64 rows a head). */
+ * at by the calls whose own kernels wait: of more than 64 rows a head, and for
+ * this one more than a few blocks of rows and keys). */
 QVG_API qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* k, const qvg_packed* v, int64_t Nk,
                                int32_t H, int32_t d, const qvg_batch* batch, const void* tables,
                                size_t tables_bytes, void* O, void* workspace, size_t ws_bytes,

@@ -330,6 +330,58 @@ def test_the_batch_agrees_with_qvg_attention(q, ora):
     assert (O[0].float() - P).abs().max() <= 2.0 ** -6 * P.abs().max()
 
 
+def test_a_recorded_timeout_and_a_failed_launch_are_reported(q, ora, monkeypatch):
+    """The status word that a kernel's expired wait would leave in the tables is
+    reported by the calls whose kernels wait, until it is read; few rows wait for
+    nothing and go on."""
+    case = Case(q, ora, seed=19, H=2, Nq=300, Nk=3000)
+    few = dict(case.args(), Q=case.Q[:, :, :2].contiguous().cuda(), q_pos=case.q_pos[:, :2].contiguous().cuda())
+    want = q.attention_batch(case.kp, case.vp, **few)
+    case.tables[:4] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8)
+    for call in (lambda: q.attention_batch(case.kp, case.vp, **case.args()), lambda: q.attention_weights(case.kp, **case.args())):
+        torch.cuda.synchronize()
+        with pytest.raises(q.QvgError) as e:
+            call()
+        assert e.value.status == 5
+    assert torch.equal(q.attention_batch(case.kp, case.vp, **few), want)
+    assert q.workspace_status(case.tables) == 5 and q.workspace_status(case.tables) == 0
+    check_attention(case, q.attention_batch(case.kp, case.vp, **case.args()))
+    monkeypatch.setenv("QVG_FAULT_INJECT", "stream")
+    w = torch.rand((2, 3000), device="cuda")
+    for call in (lambda: q.attention_batch(case.kp, case.vp, **case.args()), lambda: q.attention_weights(case.kp, **case.args()),
+                 lambda: q.evict(case.kp, case.vp, w, 100)):
+        with pytest.raises(q.QvgError) as e:
+            call()
+        assert e.value.status == 4
+    torch.cuda.synchronize()
+
+
+def test_two_threads_at_once(q, ora):
+    """Calls from two threads on streams of their own give the bits of one."""
+    import threading
+    cases = [Case(q, ora, seed=23 + i, H=2, Nq=n, Nk=2500, Nt=8, T=2, K=64) for i, n in enumerate((3, 400))]
+    args = [c.args() for c in cases]
+    call = [lambda c=c, a=a, **kw: (q.attention_batch(c.kp, c.vp, **a, **kw), q.attention_weights(c.kp, **a, **kw)) for c, a in zip(cases, args)]
+    want = [f() for f in call]
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got[i].append(call[i](stream=s))
+        s.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i in range(2):
+        assert len(got[i]) == 20
+        assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
+
+
 # ------------------------------------------------------------------ eviction
 
 def kept_plain(w, keep, first, recent):

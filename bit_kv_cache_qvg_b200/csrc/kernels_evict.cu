@@ -7,7 +7,7 @@
 // bytes and quantises nothing again: the reconstruction of a kept token is
 // the same, bit for bit.
 //
-// Two launches:
+// Two launches, or for few tokens the first alone:
 //   qvg_evict_select  a cluster of CTAs per head: a radix select finds the
 //                     weight of the last token that is kept, then one pass in
 //                     token order writes the indices of the kept ones;
@@ -25,6 +25,10 @@ constexpr int kEvBins = 2048;                     // 11 + 11 + 10 bits of a weig
 constexpr int kEvKeysSmem = 48 * 1024;            // weights of a CTA held in shared memory, at most
 constexpr int kEvCluster = 8;                     // CTAs per head, at most
 constexpr int kEvTile = 128;                      // kept tokens per gather CTA
+// Kept tokens up to which a head's one CTA gathers them, too, two threads to each:
+// 376 of 501 for 2 heads take 32.3 us a call in one launch, 34.7 in two; with a
+// thousand the gather alone in its CTAs is faster (11.8 us against 13.1).
+constexpr int kEvFused = 512;
 
 // The order of the weights as unsigned integers: larger weight, larger
 // integer; NaN below everything, the two zeros equal.
@@ -53,6 +57,7 @@ struct EvictParams {
   int H, T, ng;
   int in_smem;
   int cluster;                    // CTAs per head
+  int fused;                      // the select's CTAs gather, too
 };
 
 // Exclusive prefix sum over the CTA of two counts packed in 64 bits; *total
@@ -95,6 +100,60 @@ __device__ __forceinline__ uint2 cluster_words(const uint32_t* p, uint32_t rank)
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
   asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
   return v;
+}
+
+// A token's d/G scale (or zero) bytes.
+__device__ __forceinline__ uint4 load_row(const uint8_t* src, int n) {
+  uint4 v = make_uint4(0, 0, 0, 0);
+  switch (n) {
+    case 16: v = __ldg(reinterpret_cast<const uint4*>(src)); break;
+    case 8: { const uint2 x = __ldg(reinterpret_cast<const uint2*>(src)); v.x = x.x; v.y = x.y; break; }
+    case 4: v.x = __ldg(reinterpret_cast<const uint32_t*>(src)); break;
+    case 2: v.x = __ldg(reinterpret_cast<const uint16_t*>(src)); break;
+    default: v.x = __ldg(src);
+  }
+  return v;
+}
+__device__ __forceinline__ void store_row(uint8_t* dst, const uint4& v, int n) {
+  switch (n) {
+    case 16: *reinterpret_cast<uint4*>(dst) = v; break;
+    case 8: *reinterpret_cast<uint2*>(dst) = make_uint2(v.x, v.y); break;
+    case 4: *reinterpret_cast<uint32_t*>(dst) = v.x; break;
+    case 2: *reinterpret_cast<uint16_t*>(dst) = (uint16_t)v.x; break;
+    default: *dst = (uint8_t)v.x;
+  }
+}
+
+// Kept token i of head h, token f of the cache, by two threads (side 0 and 1):
+// each moves a half of both caches' codes and one cache's scales, zero points and
+// centroid indices, and one of them the position, the other the weight.  Everything
+// a thread reads is on its way before it writes: stores between the loads made a
+// chain of a dozen memory latencies of it.
+__device__ __forceinline__ void gather_token(const EvictParams& p, int h, int64_t i, int32_t f, int side) {
+  const int64_t out = (int64_t)h * p.keep + i, in = (int64_t)h * p.Nk + f;
+  uint4 codes[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c) codes[c] = __ldg(reinterpret_cast<const uint4*>(p.codes[c]) + 2 * in + side);
+  const uint4 scale = load_row(p.scale[side] + in * p.ng, p.ng);
+  uint4 zero = make_uint4(0, 0, 0, 0);
+  if (p.zero[side] != nullptr) zero = load_row(p.zero[side] + in * p.ng, p.ng);
+  uint8_t assign[kMaxT];
+#pragma unroll
+  for (int t = 0; t < kMaxT; ++t)
+    if (t < p.T) assign[t] = __ldg(p.assign[side] + (int64_t)t * p.H * p.Nk + in);
+  int64_t pos = f;
+  float weight = 0.0f;
+  if (side == 0 && p.pos_out != nullptr && p.k_pos != nullptr) pos = __ldg(p.k_pos + in);
+  if (side == 1 && p.weights_out != nullptr) weight = __ldg(p.weights + in);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) reinterpret_cast<uint4*>(p.codes_out[c])[2 * out + side] = codes[c];
+  store_row(p.scale_out[side] + out * p.ng, scale, p.ng);
+  if (p.zero[side] != nullptr) store_row(p.zero_out[side] + out * p.ng, zero, p.ng);
+#pragma unroll
+  for (int t = 0; t < kMaxT; ++t)
+    if (t < p.T) p.assign_out[side][(int64_t)t * p.H * p.keep + out] = assign[t];
+  if (side == 0 && p.pos_out != nullptr) p.pos_out[out] = pos;
+  if (side == 1 && p.weights_out != nullptr) p.weights_out[out] = weight;
 }
 
 // A cluster of C CTAs per head, each with a run of its tokens.  need = keep -
@@ -208,66 +267,18 @@ __global__ void __launch_bounds__(kEvThreads, 1) qvg_evict_select(const EvictPar
     if (take) out[at++] = (int32_t)i;
   }
   if (C > 1) cluster_barrier();         // no CTA leaves while another reads its counts
-}
-
-// A token's d/G scale (or zero) bytes.
-__device__ __forceinline__ uint4 load_row(const uint8_t* src, int n) {
-  uint4 v = make_uint4(0, 0, 0, 0);
-  switch (n) {
-    case 16: v = __ldg(reinterpret_cast<const uint4*>(src)); break;
-    case 8: { const uint2 x = __ldg(reinterpret_cast<const uint2*>(src)); v.x = x.x; v.y = x.y; break; }
-    case 4: v.x = __ldg(reinterpret_cast<const uint32_t*>(src)); break;
-    case 2: v.x = __ldg(reinterpret_cast<const uint16_t*>(src)); break;
-    default: v.x = __ldg(src);
-  }
-  return v;
-}
-__device__ __forceinline__ void store_row(uint8_t* dst, const uint4& v, int n) {
-  switch (n) {
-    case 16: *reinterpret_cast<uint4*>(dst) = v; break;
-    case 8: *reinterpret_cast<uint2*>(dst) = make_uint2(v.x, v.y); break;
-    case 4: *reinterpret_cast<uint32_t*>(dst) = v.x; break;
-    case 2: *reinterpret_cast<uint16_t*>(dst) = (uint16_t)v.x; break;
-    default: *dst = (uint8_t)v.x;
+  if (p.fused) {                        // one CTA to the head, few tokens: the gather, too
+    __syncthreads();
+    for (int64_t i = threadIdx.x >> 1; i < p.keep; i += kEvThreads / 2) gather_token(p, h, i, out[i], threadIdx.x & 1);
   }
 }
 
-// kEvTile kept tokens of one head, two threads to a token: each moves a half of
-// both caches' codes and one cache's scales, zero points and centroid indices,
-// and one of them the position, the other the weight.  Everything a thread reads
-// is on its way before it writes: stores between the loads made a chain of a
-// dozen memory latencies of it.
+// kEvTile kept tokens of one head, two threads to a token.
 __global__ void __launch_bounds__(2 * kEvTile) qvg_evict_gather(const EvictParams p) {
   const unsigned tiles = (unsigned)((p.keep + kEvTile - 1) / kEvTile);
-  const int h = (int)(blockIdx.x / tiles), side = threadIdx.x & 1;
+  const int h = (int)(blockIdx.x / tiles);
   const int64_t i = (int64_t)(blockIdx.x % tiles) * kEvTile + (threadIdx.x >> 1);
-  if (i >= p.keep) return;
-  const int64_t out = (int64_t)h * p.keep + i;
-  const int32_t f = __ldg(p.kept + out);
-  const int64_t in = (int64_t)h * p.Nk + f;
-  uint4 codes[2];
-#pragma unroll
-  for (int c = 0; c < 2; ++c) codes[c] = __ldg(reinterpret_cast<const uint4*>(p.codes[c]) + 2 * in + side);
-  const uint4 scale = load_row(p.scale[side] + in * p.ng, p.ng);
-  uint4 zero = make_uint4(0, 0, 0, 0);
-  if (p.zero[side] != nullptr) zero = load_row(p.zero[side] + in * p.ng, p.ng);
-  uint8_t assign[kMaxT];
-#pragma unroll
-  for (int t = 0; t < kMaxT; ++t)
-    if (t < p.T) assign[t] = __ldg(p.assign[side] + (int64_t)t * p.H * p.Nk + in);
-  int64_t pos = f;
-  float weight = 0.0f;
-  if (side == 0 && p.pos_out != nullptr && p.k_pos != nullptr) pos = __ldg(p.k_pos + in);
-  if (side == 1 && p.weights_out != nullptr) weight = __ldg(p.weights + in);
-#pragma unroll
-  for (int c = 0; c < 2; ++c) reinterpret_cast<uint4*>(p.codes_out[c])[2 * out + side] = codes[c];
-  store_row(p.scale_out[side] + out * p.ng, scale, p.ng);
-  if (p.zero[side] != nullptr) store_row(p.zero_out[side] + out * p.ng, zero, p.ng);
-#pragma unroll
-  for (int t = 0; t < kMaxT; ++t)
-    if (t < p.T) p.assign_out[side][(int64_t)t * p.H * p.keep + out] = assign[t];
-  if (side == 0 && p.pos_out != nullptr) p.pos_out[out] = pos;
-  if (side == 1 && p.weights_out != nullptr) p.weights_out[out] = weight;
+  if (i < p.keep) gather_token(p, h, i, __ldg(p.kept + (int64_t)h * p.keep + i), threadIdx.x & 1);
 }
 
 }  // namespace
@@ -289,6 +300,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   // the heads leave SMs idle and a CTA has a few thousand tokens
   p.cluster = 1;
   while (p.cluster < kEvCluster && 2 * p.cluster * p.H <= device_sm_count() && p.Nk >= 2 * p.cluster * 2048) p.cluster *= 2;
+  p.fused = p.cluster == 1 && a.keep <= kEvFused ? 1 : 0;
   const int64_t slice = (a.Nk + p.cluster - 1) / p.cluster;
   p.in_smem = slice <= kEvKeysSmem ? 1 : 0;
   const size_t smem = p.in_smem ? (size_t)slice * sizeof(uint32_t) : 0;
@@ -309,7 +321,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t s) {
   cfg.attrs = attr;
   cfg.numAttrs = p.cluster > 1 ? 1 : 0;
   if ((e = cudaLaunchKernelEx(&cfg, qvg_evict_select, p)) != cudaSuccess) return e;
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = cudaGetLastError()) != cudaSuccess || p.fused) return e;
   qvg_evict_gather<<<(unsigned)((a.keep + kEvTile - 1) / kEvTile * a.H), 2 * kEvTile, 0, s>>>(p);
   return cudaGetLastError();
 }

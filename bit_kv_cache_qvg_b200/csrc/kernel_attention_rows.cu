@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(32 * rw_warps(MT, VALUES), rw_per_sm(MT, VALUE
         L += x.y * ex2(x.x - M);
       }
       const int r = a.r0 + 16 * mt + g + 8 * i;
-      if (r < a.r1) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + r] = make_float2(M, L);
+      if (r < a.r1 && !(VALUES && p.slots == 1)) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + r] = make_float2(M, L);
     }
   }
   if (VALUES) {
@@ -389,6 +389,16 @@ __global__ void __launch_bounds__(32 * rw_warps(MT, VALUES), rw_per_sm(MT, VALUE
       for (int i = 0; i < 2; ++i) {
         const int r = a.r0 + 16 * t + g + 8 * i;
         if (r >= a.r1) continue;
+        if (p.slots == 1) {                        // nothing to join: O itself
+          float L = 0.0f;
+#pragma unroll
+          for (int w2 = 0; w2 < kGroups; ++w2) L += sml[(t + w2 * MT) * 16 + g + 8 * i].y;
+          const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+          uint32_t* row = reinterpret_cast<uint32_t*>(p.O + query_row(p, a.h, r) * kD + 8 * kNt * warp + 2 * c);
+#pragma unroll
+          for (int n = 0; n < kNt; ++n) row[4 * n] = pack2(o[t][n][2 * i] * inv, o[t][n][2 * i + 1] * inv);
+          continue;
+        }
         float* row = p.part_O + (((int64_t)a.slot * p.H + a.h) * p.R + r) * kD + 8 * kNt * warp + 2 * c;
 #pragma unroll
         for (int n = 0; n < kNt; ++n) *reinterpret_cast<float2*>(row + 8 * n) = make_float2(o[t][n][2 * i], o[t][n][2 * i + 1]);

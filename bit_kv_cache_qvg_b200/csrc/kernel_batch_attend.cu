@@ -465,7 +465,7 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
   p.slots = plan.S1 + plan.S2;
   p.slot2 = plan.S1;
   const size_t rows = (size_t)p.H * p.R;
-  if (values) p.part_O = reinterpret_cast<float*>(take(p.slots > 1 || !plan.tc1 ? p.slots * rows * kD * sizeof(float) : 0));
+  if (values) p.part_O = reinterpret_cast<float*>(take(p.slots > 1 ? p.slots * rows * kD * sizeof(float) : 0));
   p.part_ml = reinterpret_cast<float2*>(take(p.slots * rows * sizeof(float2)));
   if (!values && !plan.tc1) p.scores = reinterpret_cast<float*>(take((size_t)plan.Hn * p.R * p.Nkp * sizeof(float)));
   if (plan.tc1) {
@@ -635,9 +635,8 @@ static cudaError_t queue_attention(const BatchPlan& plan, BatchParams& p, void* 
       if ((e = launch_batch_expand(q, false, s)) != cudaSuccess) return e;
       if ((e = launch_batch_attend(q, s)) != cudaSuccess) return e;
     }
-    if (p.slots == 1) return e;
   }
-  return launch_batch_merge(p, s);
+  return p.slots == 1 ? e : launch_batch_merge(p, s);
 }
 
 static cudaError_t queue_weights(const BatchPlan& plan, BatchParams& p, const float* received, float* out, void* ws, cudaStream_t s) {

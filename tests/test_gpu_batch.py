@@ -242,6 +242,21 @@ def test_rows_that_see_nothing(q, ora, Nq):
     assert torch.count_nonzero(q.attention_weights(case.kp, **case.args())) == 0
 
 
+@pytest.mark.parametrize("kw", [dict(Nk=32), dict(Nk=64, Nq=5, B=2, group=2), dict(Nk=40, Nq=50, T=2), dict(Nk=63, Nq=300, gaps=True),
+                                dict(Nk=1, Nq=33, B=3, T=3, G=8), dict(Nk=17, B=20, group=4, T=6, K=32)],
+                         ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+def test_one_range_needs_no_joining(q, ora, kw):
+    """So few keys that a row's CTA writes O itself; some rows see nothing."""
+    B, Nq = kw.get("B", 1), kw.get("Nq", 1)
+    pos = torch.randint(0, 2 * kw["Nk"], (B, Nq), generator=torch.Generator().manual_seed(2))
+    if Nq > 1:
+        pos[:, ::4] = -3
+    case = Case(q, ora, seed=29, causal=True, q_pos=pos, **kw)
+    case.tables = q.rope_tables(4 * kw["Nk"] + 100)     # to cover every position above
+    check_attention(case, q.attention_batch(case.kp, case.vp, **case.args()))
+    check_weights(case, q.attention_weights(case.kp, **case.args()))
+
+
 @pytest.mark.parametrize("Nq", [1, 300, 1500])
 def test_large_scores_and_far_positions(q, ora, Nq):
     """Scores of several tens (a weight near 1 at one key), and a cache whose

@@ -102,6 +102,13 @@ __device__ __forceinline__ int64_t query_pos(const BatchParams& p, int64_t r) {
 __device__ __forceinline__ int row_limit(const BatchParams& p, int64_t pos) {
   return pos < 0 ? kLimitNone : p.causal ? clamp_pos(pos) : kLimitAll;
 }
+// The limit of a row that sees no key, for the sums by key: its logarithm of +inf
+// takes every finite score to a weight of 0, without a mask, and the operands of
+// padding rows and behind the last row are zeros.  The queries of a causal row
+// before every key may be anything: that one is masked.
+__device__ __forceinline__ int unseen_limit(const BatchParams& p, int64_t pos) {
+  return p.causal && pos >= 0 ? kLimitNone : kLimitAll;
+}
 __device__ __forceinline__ int64_t tail_length(const BatchParams& p, int b) {
   const int64_t n = p.tail_len != nullptr ? (int64_t)__ldg(p.tail_len + b) : p.Nt;
   return n < 0 ? 0 : n < p.Nt ? n : p.Nt;

@@ -29,7 +29,8 @@ constexpr int kExKeys = kExThreads / 8;           // keys per pass
 constexpr int kExPasses = kAtTile / kExKeys;
 
 // 128 rows of a head, or of one sequence, rotated at their positions; zeros
-// behind the last one.
+// behind the last one and for padding rows, whatever their queries hold: the
+// sums by key take every row's scores, and 2^(x - inf) is 0 for a finite x only.
 template <bool PRECISE>
 __device__ __forceinline__ void expand_rows(const BatchParams& p, bool by_sequence, int hl, int b, int64_t tile) {
   const int which = by_sequence ? 1 : 0;
@@ -42,8 +43,10 @@ __device__ __forceinline__ void expand_rows(const BatchParams& p, bool by_sequen
     uint4 hi = make_uint4(0, 0, 0, 0), lo = hi;
     if (r < rows) {
       const int64_t row = by_sequence ? b * p.RB + r : r;
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.Q + query_row(p, p.h0 + hl, row) * kD + 8 * cb));
-      turn_chunk<PRECISE>(p.rope + rope_row(p, query_pos(p, row)) * (kD / 2) + 4 * cb, x, hi, lo);
+      const int64_t pos = query_pos(p, row);
+      uint4 x = __ldg(reinterpret_cast<const uint4*>(p.Q + query_row(p, p.h0 + hl, row) * kD + 8 * cb));
+      if (pos < 0) x = make_uint4(0, 0, 0, 0);
+      turn_chunk<PRECISE>(p.rope + rope_row(p, pos) * (kD / 2) + 4 * cb, x, hi, lo);
     }
     const int64_t at = (base + (cb >> 3) * pad + r) * 128 + (((cb & 7) ^ (int)(r & 7)) << 4);
     *reinterpret_cast<uint4*>(p.row_img[which] + at) = hi;

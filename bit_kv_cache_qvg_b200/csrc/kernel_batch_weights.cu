@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
       const bool seen = limit != kLimitNone && total != 0.0f;
       const int64_t at = (int64_t)a.hl * p.Rp + mine;
       p.lse[at] = seen ? m_run + log2f(total) : INFINITY;
-      p.limits[at] = seen ? limit : kLimitAll;
+      p.limits[at] = seen ? limit : in ? unseen_limit(p, query_pos(p, mine)) : kLimitAll;
     }
     if (ok && in && side == 0) {
       if (STATS) {
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
 
 // The rows' lse from the partial results, and their limits, for the second
 // pass: lse = +inf (every weight 0) for a row that sees nothing and behind the
-// last row, whose limits then ask for no mask.
+// last row.
 __global__ void __launch_bounds__(256) qvg_batch_lse(const BatchParams p, float* lse, int* limits) {
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (e >= p.Hn * p.Rp) return;
@@ -397,9 +397,11 @@ __global__ void __launch_bounds__(256) qvg_batch_lse(const BatchParams p, float*
       const float2 ml = __ldg(p.part_ml + s * stride + row);
       L += ml.y * exp2_approx(ml.x - M);
     }
+    const int64_t pos = query_pos(p, r);
+    limit = unseen_limit(p, pos);
     if (L != 0.0f) {
       x = M + log2f(L);
-      limit = row_limit(p, query_pos(p, r));
+      limit = row_limit(p, pos);
     }
   }
   lse[e] = x;

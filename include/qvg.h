@@ -342,7 +342,7 @@ QVG_API size_t qvg_attention_workspace_bytes(const qvg_config* cfg, int64_t Nk, 
  *   Q         [B][H * group][Nq][d] bf16, before the rotary embedding; query
  *             heads h * group .. h * group + group - 1 read K/V head h
  *   q_pos     [B][Nq] positions; a negative one marks a padding row, which
- *             sees no key
+ *             sees no key and whose query may hold anything
  *   k_pos     [H][Nk] positions of the cached tokens (as qvg_evict leaves
  *             them), in any order; NULL: token i at position i
  *   Nt        tokens of room in each sequence's tail, its own newest tokens,

@@ -242,6 +242,30 @@ def test_rows_that_see_nothing(q, ora, Nq):
     assert torch.count_nonzero(q.attention_weights(case.kp, **case.args())) == 0
 
 
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("Nq", [2, 40, 300])
+@pytest.mark.parametrize("fill", [float("nan"), float("inf")])
+def test_padding_rows_may_hold_anything(q, ora, Nq, causal, fill):
+    """Queries of padding rows that nobody wrote, and of rows before every key:
+    the other rows and the weights are what they are without them."""
+    pos = torch.arange(Nq).repeat(2, 1) + 700
+    pos[0, 0], pos[1, Nq // 2:] = -1, -5
+    case = Case(q, ora, seed=41, H=2, B=2, Nq=Nq, Nk=700, Nt=6, causal=causal, q_pos=pos, group=2, T=2)
+    if causal:                                          # a row before every key: the cache moved behind it
+        case.k_pos = torch.arange(case.Nk).repeat(case.H, 1) + 3
+        case.tail_pos = case.tail_pos + 3
+        case.tail.pos = case.tail_pos.cuda()
+        pos[0, 1] = 2
+    calls = (lambda: q.attention_batch(case.kp, case.vp, **case.args()), lambda: q.attention_weights(case.kp, **case.args()))
+    O, W = (f() for f in calls)
+    check_attention(case, O)
+    check_weights(case, W)
+    unseen = (pos < 0) | (causal & (pos < 3))
+    case.Q = torch.where(unseen[:, None, :, None], fill, case.Q)
+    O2, W2 = (f() for f in calls)
+    assert torch.equal(O, O2) and torch.equal(W, W2)
+
+
 @pytest.mark.parametrize("kw", [dict(Nk=32), dict(Nk=64, Nq=5, B=2, group=2), dict(Nk=40, Nq=50, T=2), dict(Nk=63, Nq=300, gaps=True),
                                 dict(Nk=1, Nq=33, B=3, T=3, G=8), dict(Nk=17, B=20, group=4, T=6, K=32)],
                          ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))

@@ -6,6 +6,7 @@ missing, every call raises ``QvgError`` -- there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -411,14 +412,33 @@ def _same_kind(kp: Packed, vp: Packed):
         raise QvgError(1, "kp and vp must have the same sizes and configuration")
 
 
-def _lent(stream, *tensors):
-    """Tensors allocated here on the current stream whose work runs on `stream`:
-    their memory is not reused before that work is done."""
+def _torch_stream(stream, dev):
+    """`stream` (a torch stream or a handle) as a torch stream of `dev`."""
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != dev:
+            raise QvgError(1, f"the stream must be one of {dev}")
+        return stream
+    handle = int(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _memory(stream, dev):
+    """Memory for work on `stream` (None: the current one) comes from that stream's
+    own blocks: a block that the current stream has let go of may still be in use
+    by what is queued there, and nothing orders `stream` behind it."""
+    return _CURRENT if stream is None else torch.cuda.stream(_torch_stream(stream, dev))
+
+
+def _returned(stream, dev, *tensors):
+    """Tensors allocated for `stream` that the caller gets: not reused before what
+    the caller's current stream has queued when they are freed."""
     if stream is not None:
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream))
+        s = torch.cuda.current_stream(dev)
         for t in tensors:
-            if t.numel():
-                t.record_stream(s)
+            t.record_stream(s)
 
 
 def _queue(dev, stream, call, *args) -> int:
@@ -436,8 +456,8 @@ def _workspace(workspace, size_call, p: Packed, b: _Batch, dev, stream) -> torch
         else:
             with torch.cuda.device(dev):
                 need = size_call(C.byref(p.cfg), p.N, p.H, C.byref(b))
-        workspace = p.codes.new_empty(need)
-        _lent(stream, workspace)
+        with _memory(stream, dev):
+            workspace = p.codes.new_empty(need)
     elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
         raise QvgError(1, f"the workspace must be a contiguous uint8 tensor on {dev}")
     return workspace
@@ -466,8 +486,9 @@ def attention_batch(kp: Packed, vp: Packed, Q: torch.Tensor, q_pos: torch.Tensor
     L = lib()
     ws = _workspace(workspace, L.qvg_attention_batch_workspace_bytes, kp, b, dev, stream)
     if O is None:
-        O = torch.empty_like(Q)
-        _lent(stream, O)
+        with _memory(stream, dev):
+            O = torch.empty_like(Q)
+        _returned(stream, dev, O)
     _check(_queue(dev, stream, L.qvg_attention_batch, C.byref(kp.cfg), C.byref(kp.struct()), C.byref(vp.struct()), kp.N, kp.H, kp.d,
                   C.byref(b), tables.data_ptr(), tables.numel(), O.data_ptr(), ws.data_ptr(), ws.numel()), "qvg_attention_batch")
     return O
@@ -489,8 +510,9 @@ def attention_weights(kp: Packed, Q: torch.Tensor, q_pos: torch.Tensor, tables: 
     L = lib()
     ws = _workspace(workspace, L.qvg_attention_weights_workspace_bytes, kp, b, dev, stream)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=dev)
-        _lent(stream, out)
+        with _memory(stream, dev):
+            out = torch.empty(shape, dtype=torch.float32, device=dev)
+        _returned(stream, dev, out)
     _check(_queue(dev, stream, L.qvg_attention_weights, C.byref(kp.cfg), C.byref(kp.struct()), kp.N, kp.H, kp.d, C.byref(b),
                   tables.data_ptr(), tables.numel(), before, out.data_ptr(), ws.data_ptr(), ws.numel()),
            "qvg_attention_weights")
@@ -554,12 +576,12 @@ def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int =
     at_w = _device_tensor(weights, "weights", torch.float32, shape, dev)
     at_pos = _device_tensor(k_pos, "k_pos", torch.int64, shape, dev)
     _on_device(kp.codes, vp.codes)
-    k, v = _closed(kp, vp, keep)
     shape = (kp.H, keep)
     new = weights.new_empty
-    e = Evicted(k, v, new(shape, dtype=torch.int32), new(shape, dtype=torch.int64), new(shape))
-    if stream is not None:
-        _lent(stream, e.kept, e.pos, e.weights, *(t for p in (e.k, e.v) for t in (p.codes, p.scale, p.zero, p.assign)))
+    with _memory(stream, dev):
+        k, v = _closed(kp, vp, keep)
+        e = Evicted(k, v, new(shape, dtype=torch.int32), new(shape, dtype=torch.int64), new(shape))
+    _returned(stream, dev, e.kept, e.pos, e.weights, k.codes)       # both caches' streams are one allocation
     _check(_queue(dev, stream, lib().qvg_evict, C.byref(kp.cfg), C.byref(kp.struct()), C.byref(vp.struct()), kp.N, kp.H, kp.d, at_w,
                   at_pos, keep, first, recent, C.byref(e.k.struct()), C.byref(e.v.struct()), e.kept.data_ptr(),
                   e.pos.data_ptr(), e.weights.data_ptr()), "qvg_evict")

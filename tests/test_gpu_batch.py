@@ -421,6 +421,42 @@ def test_two_threads_at_once(q, ora):
         assert all(torch.equal(a, b) for r in got[i] for a, b in zip(r, want[i]))
 
 
+@pytest.mark.parametrize("Nq", [1, 24, 400])
+def test_a_side_stream_leaves_the_current_one_s_blocks_alone(q, ora, Nq):
+    """A block that the current stream has let go of while its work is still
+    queued is not what a call on another stream gets; the results are those of
+    the current stream, with work of both queued at once."""
+    case = Case(q, ora, seed=47, B=2, Nq=Nq, Nk=3000, Nt=8, T=2, K=64)
+    args = case.args()
+    w = torch.rand((case.H, case.Nk), device="cuda")
+    calls = [lambda **kw: q.attention_batch(case.kp, case.vp, **args, **kw), lambda **kw: q.attention_weights(case.kp, **args, **kw),
+             lambda **kw: q.evict(case.kp, case.vp, w, 1500, **kw).k.codes]
+    want = [f() for f in calls]
+    sizes = (case.cfg, case.Nk, case.H, case.B, case.group, case.Nq, case.Nt)
+    need = (q.attention_batch_workspace_bytes(*sizes), q.attention_weights_workspace_bytes(*sizes), 1 << 20)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for f, r, n in zip(calls, want, need):
+        held = torch.empty(n, dtype=torch.uint8, device="cuda")
+        at = held.data_ptr()
+        torch.cuda._sleep(2_000_000)
+        held.fill_(255)
+        del held
+        got = f(stream=side)
+        assert not at <= got.data_ptr() < at + n
+        assert torch.empty(n, dtype=torch.uint8, device="cuda").data_ptr() == at      # it is still the current stream's
+        torch.cuda.synchronize()
+        assert torch.equal(got, r)
+    for _ in range(10):                                 # both streams, and results freed while they are read
+        a = [f() for f in calls]
+        b = [f(stream=side) for f in calls]
+        c = [f(stream=side.cuda_stream) for f in calls]
+        torch.cuda.current_stream().wait_stream(side)
+        same = [torch.equal(x, r) for g in (a, b, c) for x, r in zip(g, want)]
+        del a, b, c
+        assert all(same)
+
+
 # ------------------------------------------------------------------ eviction
 
 def kept_plain(w, keep, first, recent):

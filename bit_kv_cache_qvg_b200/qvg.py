@@ -173,6 +173,36 @@ def _stream(stream) -> Optional[int]:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _torch_stream(stream, dev):
+    """`stream` (a torch stream or a handle) as a torch stream of `dev`."""
+    if isinstance(stream, torch.cuda.Stream):
+        if dev.index is not None and stream.device != dev:
+            raise QvgError(1, f"the stream must be one of {dev}")
+        return stream
+    handle = int(getattr(stream, "cuda_stream", stream))
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
+_CURRENT = contextlib.nullcontext()
+
+
+def _memory(stream, dev):
+    """Memory for work on `stream` (None: the current one) comes from that stream's
+    own blocks: a block that the current stream has let go of may still be in use
+    by what is queued there, and nothing orders `stream` behind it."""
+    return _CURRENT if stream is None else torch.cuda.stream(_torch_stream(stream, dev))
+
+
+def _returned(stream, dev, *tensors):
+    """Tensors allocated for `stream` that the caller gets: not reused before what
+    the caller's current stream has queued when they are freed."""
+    if stream is not None:
+        s = torch.cuda.current_stream(dev)
+        for t in tensors:
+            if t.numel():
+                t.record_stream(s)
+
+
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -250,6 +280,14 @@ def alloc_workspace(cfg: Config, N: int, H: int, d: int = 128, dtype: int = BF16
     return ws
 
 
+def _new_packed(cfg: Config, N: int, H: int, d: int, dtype: int, dev, stream) -> Packed:
+    """alloc_packed for the result of work on `stream`."""
+    with _memory(stream, dev):
+        p = alloc_packed(cfg, N, H, d, dtype, dev)
+    _returned(stream, dev, p.codes, p.scale, p.zero, p.assign, p.centroids)
+    return p
+
+
 def quantize(X: torch.Tensor, cfg: Config, init: Optional[torch.Tensor] = None,
              out: Optional[Packed] = None, workspace: Optional[torch.Tensor] = None,
              stream=None) -> Packed:
@@ -259,9 +297,10 @@ def quantize(X: torch.Tensor, cfg: Config, init: Optional[torch.Tensor] = None,
     H, N, d = X.shape
     dt = _DTYPES[X.dtype]
     if out is None:
-        out = alloc_packed(cfg, N, H, d, dt, X.device)
+        out = _new_packed(cfg, N, H, d, dt, X.device, stream)
     if workspace is None:
-        workspace = alloc_workspace(cfg, N, H, d, dt, X.device)
+        with _memory(stream, X.device):
+            workspace = alloc_workspace(cfg, N, H, d, dt, X.device)
     ps = out.struct()
     st = lib().qvg_quantize(C.byref(cfg), _ptr(X), dt, N, H, d, _ptr(init), C.byref(ps),
                             _ptr(workspace), workspace.numel(), _stream(stream))
@@ -278,7 +317,7 @@ def quantize_static(X: torch.Tensor, cfg: Config, init: Optional[torch.Tensor] =
     H, N, d = X.shape
     dt = _DTYPES[X.dtype]
     if out is None:
-        out = alloc_packed(cfg, N, H, d, dt, X.device)
+        out = _new_packed(cfg, N, H, d, dt, X.device, stream)
     ps = out.struct()
     st = lib().qvg_quantize_static(C.byref(cfg), _ptr(X), dt, N, H, d, _ptr(init), C.byref(ps), _stream(stream))
     _check(st, "qvg_quantize_static")
@@ -287,7 +326,9 @@ def quantize_static(X: torch.Tensor, cfg: Config, init: Optional[torch.Tensor] =
 
 def dequantize(p: Packed, Y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     if Y is None:
-        Y = torch.empty((p.H, p.N, p.d), dtype=_TORCH[p.dtype], device=p.codes.device)
+        with _memory(stream, p.codes.device):
+            Y = torch.empty((p.H, p.N, p.d), dtype=_TORCH[p.dtype], device=p.codes.device)
+        _returned(stream, p.codes.device, Y)
     ps = p.struct()
     st = lib().qvg_dequantize(C.byref(p.cfg), C.byref(ps), p.dtype, p.N, p.H, p.d, _ptr(Y), _stream(stream))
     _check(st, "qvg_dequantize")
@@ -300,7 +341,10 @@ def rope_tables(max_pos: int, base: float = 10000.0, d: int = 128, device="cuda"
     n = int(lib().qvg_rope_tables_bytes(d, max_pos))
     if n == 0:
         raise QvgError(1, "qvg_rope_tables_bytes")
-    t = torch.empty(n, dtype=torch.uint8, device=device)
+    device = torch.device(device)
+    with _memory(stream, device):
+        t = torch.empty(n, dtype=torch.uint8, device=device)
+    _returned(stream, device, t)
     _check(lib().qvg_rope_tables(float(base), d, max_pos, _ptr(t), n, _stream(stream)), "qvg_rope_tables")
     return t
 
@@ -316,10 +360,13 @@ def attention(kp: Packed, vp: Packed, Q: torch.Tensor, q_pos: torch.Tensor, tabl
         raise QvgError(1, "Q must be a contiguous bf16 [H][Nq][d] tensor")
     H, Nq, d = Q.shape
     if O is None:
-        O = torch.empty((H, Nq, d), dtype=torch.float32, device=Q.device)
+        with _memory(stream, Q.device):
+            O = torch.empty((H, Nq, d), dtype=torch.float32, device=Q.device)
+        _returned(stream, Q.device, O)
     if workspace is True:
         n = attention_workspace_bytes(kp.cfg, kp.N, H, Nq)
-        workspace = torch.empty(n, dtype=torch.uint8, device=Q.device) if n > 0 else None
+        with _memory(stream, Q.device):
+            workspace = torch.empty(n, dtype=torch.uint8, device=Q.device) if n > 0 else None
     ws_ptr, ws_n = (_ptr(workspace), workspace.numel()) if workspace is not None else (None, 0)
     ks, vs = kp.struct(), vp.struct()
     _check(lib().qvg_attention(C.byref(kp.cfg), C.byref(ks), C.byref(vs), kp.N, H, d, _ptr(Q),
@@ -410,35 +457,6 @@ def _same_kind(kp: Packed, vp: Packed):
     if vp.N != kp.N or vp.H != kp.H or vp.d != kp.d or vp.dtype != kp.dtype or \
             (vp.cfg is not kp.cfg and bytes(vp.cfg) != bytes(kp.cfg)):
         raise QvgError(1, "kp and vp must have the same sizes and configuration")
-
-
-def _torch_stream(stream, dev):
-    """`stream` (a torch stream or a handle) as a torch stream of `dev`."""
-    if isinstance(stream, torch.cuda.Stream):
-        if stream.device != dev:
-            raise QvgError(1, f"the stream must be one of {dev}")
-        return stream
-    handle = int(getattr(stream, "cuda_stream", stream))
-    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
-
-
-_CURRENT = contextlib.nullcontext()
-
-
-def _memory(stream, dev):
-    """Memory for work on `stream` (None: the current one) comes from that stream's
-    own blocks: a block that the current stream has let go of may still be in use
-    by what is queued there, and nothing orders `stream` behind it."""
-    return _CURRENT if stream is None else torch.cuda.stream(_torch_stream(stream, dev))
-
-
-def _returned(stream, dev, *tensors):
-    """Tensors allocated for `stream` that the caller gets: not reused before what
-    the caller's current stream has queued when they are freed."""
-    if stream is not None:
-        s = torch.cuda.current_stream(dev)
-        for t in tensors:
-            t.record_stream(s)
 
 
 def _queue(dev, stream, call, *args) -> int:
@@ -687,7 +705,10 @@ class Cache:
 
     def dequantize(self, Y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         if Y is None:
-            Y = torch.empty((self.H, self.tokens, self.d), dtype=_TORCH[self.dtype], device="cuda")
+            device = torch.device("cuda")
+            with _memory(stream, device):
+                Y = torch.empty((self.H, self.tokens, self.d), dtype=_TORCH[self.dtype], device=device)
+            _returned(stream, device, Y)
         _check(lib().qvg_cache_dequantize(self._h, _ptr(Y), _stream(stream)), "qvg_cache_dequantize")
         return Y
 

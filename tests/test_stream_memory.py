@@ -7,7 +7,6 @@ blocks, and what it returns is kept from reuse until the caller's stream is done
 with it.  Without a GPU: torch's streams and the library are stand-ins that note
 what is done on which stream."""
 import contextlib
-import ctypes as C
 
 import pytest
 import torch
@@ -73,16 +72,19 @@ def calls(q):
     kp, vp = q.alloc_packed(cfg, 100, 2, device="cpu"), q.alloc_packed(cfg, 100, 2, device="cpu")
     Q, pos = torch.zeros((1, 4, 3, 128), dtype=torch.bfloat16), torch.zeros((1, 3), dtype=torch.int64)
     tables, w, X = torch.zeros(256 + 512 * 200, dtype=torch.uint8), torch.zeros((2, 100)), torch.zeros((2, 100, 128))
-    cache = q.Cache.__new__(q.Cache)
-    cache._h, cache.H, cache.d, cache.dtype, cache.cfg, cache.policy = C.c_void_p(), 2, 128, q.FP32, cfg, None
     return dict(
         attention_batch=lambda s: q.attention_batch(kp, vp, Q, pos, tables, stream=s),
         attention_weights=lambda s: q.attention_weights(kp, Q, pos, tables, stream=s),
         evict=lambda s: q.evict(kp, vp, w, 40, stream=s),
+        quantize=lambda s: q.quantize(X, cfg, stream=s),
+        quantize_static=lambda s: q.quantize_static(X, cfg, stream=s),
+        dequantize=lambda s: q.dequantize(kp, stream=s),
+        rope_tables=lambda s: q.rope_tables(10, device="cpu", stream=s),
+        attention=lambda s: q.attention(kp, vp, Q[0], pos[0], tables, stream=s),
     )
 
 
-NEW = ["attention_batch", "attention_weights", "evict"]
+CALLS = ["attention_batch", "attention_weights", "evict", "quantize", "quantize_static", "dequantize", "rope_tables", "attention"]
 
 
 def tensors(x):
@@ -91,7 +93,7 @@ def tensors(x):
     return [t for v in vars(x).values() if isinstance(v, torch.Tensor) or hasattr(v, "codes") for t in tensors(v)]
 
 
-@pytest.mark.parametrize("name", NEW)
+@pytest.mark.parametrize("name", CALLS)
 @pytest.mark.parametrize("stream", [Side(), 78, 0], ids=["stream", "handle", "default"])
 def test_memory_belongs_to_the_stream_of_the_work(q, name, stream):
     call = calls(q)[name]
@@ -107,7 +109,7 @@ def test_memory_belongs_to_the_stream_of_the_work(q, name, stream):
     assert q.world["stream"] == CALLER
 
 
-@pytest.mark.parametrize("name", NEW)
+@pytest.mark.parametrize("name", CALLS)
 def test_without_a_stream_it_is_the_current_one_s(q, name, monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0)
     monkeypatch.setattr(q, "_stream", lambda s: 0)

@@ -242,9 +242,27 @@ class Packed:
     dtype: int
 
     def struct(self) -> _Packed:
-        # an empty tensor's address is 0
+        """The tensors' addresses (0 for an empty one).  The library takes them as
+        contiguous arrays of these sizes: a tensor that is not one is refused."""
+        cfg, T, tokens = self.cfg, self.cfg.T, self.H * self.N
+        device, groups = self.codes.get_device(), tokens * (self.d // max(cfg.group_size, 1))
+        self._check("codes", self.codes, tokens * self.d // 4, device)
+        self._check("scale", self.scale, groups, device)
+        if cfg.scale_mode == ASYM:
+            self._check("zero", self.zero, groups, device)
+        if T > 0:
+            self._check("assign", self.assign, T * tokens, device)
+            self._check("centroids", self.centroids, T * self.H * cfg.K * self.d * (2 if self.dtype == BF16 else 4), device)
+        return self._addresses()
+
+    def _addresses(self) -> _Packed:
         return _Packed(self.codes.data_ptr(), self.scale.data_ptr(), self.zero.data_ptr(), self.assign.data_ptr(),
                        self.centroids.data_ptr())
+
+    @staticmethod
+    def _check(name: str, t: torch.Tensor, size: int, device: int):
+        if t.nbytes != size or not t.is_contiguous() or t.get_device() != device:
+            raise QvgError(1, f"{name} must be a contiguous tensor of {size} bytes on the device of codes")
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
@@ -594,14 +612,15 @@ def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int =
     at_w = _device_tensor(weights, "weights", torch.float32, shape, dev)
     at_pos = _device_tensor(k_pos, "k_pos", torch.int64, shape, dev)
     _on_device(kp.codes, vp.codes)
+    ks, vs = kp.struct(), vp.struct()
     shape = (kp.H, keep)
     new = weights.new_empty
     with _memory(stream, dev):
         k, v = _closed(kp, vp, keep)
         e = Evicted(k, v, new(shape, dtype=torch.int32), new(shape, dtype=torch.int64), new(shape))
     _returned(stream, dev, e.kept, e.pos, e.weights, k.codes)       # both caches' streams are one allocation
-    _check(_queue(dev, stream, lib().qvg_evict, C.byref(kp.cfg), C.byref(kp.struct()), C.byref(vp.struct()), kp.N, kp.H, kp.d, at_w,
-                  at_pos, keep, first, recent, C.byref(e.k.struct()), C.byref(e.v.struct()), e.kept.data_ptr(),
+    _check(_queue(dev, stream, lib().qvg_evict, C.byref(kp.cfg), C.byref(ks), C.byref(vs), kp.N, kp.H, kp.d, at_w,
+                  at_pos, keep, first, recent, C.byref(k._addresses()), C.byref(v._addresses()), e.kept.data_ptr(),
                   e.pos.data_ptr(), e.weights.data_ptr()), "qvg_evict")
     return e
 

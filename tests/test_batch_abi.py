@@ -162,3 +162,71 @@ def test_the_binding_checks_before_it_calls(q):
     with pytest.raises(q.QvgError) as e:
         q.attention_weights(q.alloc_packed(cfg, 100, 2, dtype=q.FP32, device="cpu"), Q, pos, tables)
     assert e.value.status == 2
+
+
+# ------------------------------------------------------------------ packed streams
+
+def damaged(q, cfg, H=2, N=100):
+    """A packed form, and what one of its tensors could be that is not laid out as its sizes say."""
+    import dataclasses
+    p = q.alloc_packed(cfg, N, H, device="cpu")
+    wide = q.alloc_packed(cfg, N, 2 * H, device="cpu")
+    tall = q.alloc_packed(cfg, 2 * N, H, device="cpu")
+    for name in ("codes", "scale", "zero", "assign", "centroids"):
+        if getattr(p, name).numel() == 0:
+            continue
+        by_head = 1 if name in ("assign", "centroids") else 0
+        every_other = torch.narrow(getattr(wide, name), by_head, 0, 2 * H).unflatten(by_head, (H, 2)).select(by_head + 1, 0)
+        yield name, dataclasses.replace(p, **{name: every_other})              # heads with a gap between them
+        yield name, dataclasses.replace(p, **{name: getattr(p, name).narrow(by_head, 0, H - 1)})          # a head short
+        if name != "centroids":
+            part = getattr(tall, name).narrow(by_head + 1, 0, N)              # a part of longer streams
+            assert part.shape == getattr(p, name).shape
+            yield name, dataclasses.replace(p, **{name: part})
+            yield name, dataclasses.replace(p, **{name: getattr(tall, name)})
+        yield name, dataclasses.replace(p, **{name: getattr(p, name).float()})
+
+
+@pytest.mark.parametrize("T,mode", [(2, 0), (1, 1), (0, 0)])
+def test_packed_streams_that_are_not_laid_out_as_their_sizes_say_are_refused(q, T, mode, monkeypatch):
+    """Every call reads (or writes) a packed form's tensors as contiguous arrays of its
+    sizes: a strided view, a short or a long one, another element size is refused
+    before the library is called."""
+    cfg = q.config(K=16, T=T, group_size=64, scale_mode=mode)
+    good = q.alloc_packed(cfg, 100, 2, device="cpu")
+    good.struct()
+    Q, pos = torch.zeros((1, 4, 3, 128), dtype=torch.bfloat16), torch.zeros((1, 3), dtype=torch.int64)
+    tables, w, X = torch.zeros(256 + 512 * 200, dtype=torch.uint8), torch.zeros((2, 100)), torch.zeros((2, 100, 128), dtype=torch.bfloat16)
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*a):
+                assert name.endswith("_bytes"), f"{name} was called"
+                return 4096
+            return call
+
+    monkeypatch.setattr(q, "lib", Library)
+    monkeypatch.setattr(q, "_on_device", lambda *t: torch.device("cpu"))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 0)
+    monkeypatch.setattr(q, "_stream", lambda s: 0)
+    n = 0
+    for name, p in damaged(q, cfg):
+        for call in (lambda: q.attention_batch(p, good, Q, pos, tables), lambda: q.attention_batch(good, p, Q, pos, tables),
+                     lambda: q.attention_weights(p, Q, pos, tables), lambda: q.evict(p, good, w, 50), lambda: q.evict(good, p, w, 50),
+                     lambda: q.attention(p, good, Q[0, :2], pos[0], tables), lambda: q.dequantize(p),
+                     lambda: q.quantize(X, cfg, out=p, workspace=torch.zeros(4096, dtype=torch.uint8)), lambda: q.quantize_static(X, cfg, out=p)):
+            with pytest.raises(q.QvgError) as e:
+                call()
+            assert e.value.status == 1 and name in str(e.value), (name, str(e.value))
+            n += 1
+    assert n > 50
+
+
+def test_heads_of_a_packed_form_that_are_contiguous_are_taken(q):
+    """A part whose strides say no more than its sizes is a packed form."""
+    p = q.alloc_packed(q.config(K=16, T=1, group_size=64), 100, 5, device="cpu")
+    one = q.Packed(codes=p.codes[-2:], scale=p.scale[-2:], zero=p.zero[-2:], assign=p.assign[:, -2:], centroids=p.centroids[:, -2:],
+                   cfg=p.cfg, N=100, H=2, d=128, dtype=q.BF16)
+    s = one.struct()
+    assert s.codes == p.codes.data_ptr() + 3 * 100 * 32 and s.assign == p.assign.data_ptr() + 300

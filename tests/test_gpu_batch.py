@@ -395,6 +395,19 @@ def test_a_recorded_timeout_and_a_failed_launch_are_reported(q, ora, monkeypatch
     torch.cuda.synchronize()
 
 
+def test_packed_streams_on_another_device_are_refused(q, ora):
+    import dataclasses
+    case = Case(q, ora, seed=53, H=2, Nk=200, T=2)
+    w = torch.rand((2, 200), device="cuda")
+    for name in ("scale", "zero", "assign", "centroids"):
+        p = dataclasses.replace(case.kp, **{name: getattr(case.kp, name).cpu()})
+        for call in (lambda: q.attention_batch(p, case.vp, **case.args()), lambda: q.attention_batch(case.kp, p, **case.args()),
+                     lambda: q.attention_weights(p, **case.args()), lambda: q.evict(p, case.vp, w, 50), lambda: q.dequantize(p)):
+            with pytest.raises(q.QvgError) as e:
+                call()
+            assert e.value.status == 1 and name in str(e.value)
+
+
 def test_two_threads_at_once(q, ora):
     """Calls from two threads on streams of their own give the bits of one."""
     import threading

@@ -37,6 +37,7 @@ struct __align__(16) WtShared {
   uint64_t drained;
   uint32_t tmem_base;
   int abort_flag;
+  int failed;                     // second pass: a wait had run out before this launch
 };
 
 // What a CTA has to do.  First pass (STATS): rows r0 .. of head h over tiles
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
   uint8_t* ring = own + 4 * kAtOpBytes;
   WtShared* sh = reinterpret_cast<WtShared*>(ring + kWtSlots * kAtOpBytes);
   volatile int* abort_flag = &sh->abort_flag;
-  const WtPlace a = wt_place<STATS>(p);
+  WtPlace a = wt_place<STATS>(p);
   const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -110,6 +111,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
       bar_init(&sh->v_free[i], (uint32_t)(a.groups * 8));
     }
     sh->abort_flag = 0;
+    sh->failed = !STATS && *static_cast<const volatile uint32_t*>(p.status) != 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 0) {
@@ -119,6 +121,9 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
   fence_before();
   __syncthreads();
   fence_after();
+  // After a wait that ran out (in the first pass above all) the rows' logarithms may
+  // be anything: no rows then, so that every key keeps what it received before.
+  if (!STATS && sh->failed) a.steps = 0;
   const uint32_t tmem = uniform(sh->tmem_base);              // scores of resident tile g in buffer i at column 256 g + 128 i
 
   if (warp == 17) {
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
     float2* half = reinterpret_cast<float2*>(own + 2 * g * kAtOpBytes) + (threadIdx.x & 127);
     if (STATS) {
       if (side == 1) *half = make_float2(m_run, total);
-      named_bar_or(1 + g, 256, false);
+      ok = !named_bar_or(1 + g, 256, !ok);
       if (side == 0) {
         const float2 other = *half;
         const float M = fmaxf(m_run, other.x);
@@ -350,8 +355,8 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
       }
     } else {
       if (side == 1) half->x = total;
-      named_bar_or(1 + g, 256, false);
-      if (side == 0) total += half->x;
+      ok = !named_bar_or(1 + g, 256, !ok);
+      if (side == 0) total = ok ? total + half->x : 0.0f;          // after a failed wait: nothing is added
     }
     // a single range: nothing for qvg_batch_lse to join
     if (STATS && ok && side == 0 && p.slots == 1) {
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
       p.lse[at] = seen ? m_run + log2f(total) : INFINITY;
       p.limits[at] = seen ? limit : in ? unseen_limit(p, query_pos(p, mine)) : kLimitAll;
     }
-    if (ok && in && side == 0) {
+    if ((ok || !STATS) && in && side == 0) {
       if (STATS) {
         if (p.slots > 1) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + mine] = make_float2(m_run, limit == kLimitNone ? 0.0f : total);
       } else if (p.row_cuts > 1) {

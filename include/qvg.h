@@ -408,7 +408,10 @@ QVG_API qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* 
  * saturate) and every sum in fp32, in an order that does not depend on the
  * launch, so equal calls give equal bits.
  *   received  DEVICE [H][Nk] fp32, or NULL: zeros
- *   out       DEVICE [H][Nk] fp32; may be `received` itself
+ *   out       DEVICE [H][Nk] fp32; may be `received` itself.  After a recorded
+ *             timeout (of this call or of earlier work) every token's out is its sum or
+ *             what it had received: a call in a captured graph, or on a stream with work
+ *             queued, adds nothing until the status is read and cleared
  * Only `k` of the cache is read.  Workspace and errors as qvg_attention_batch. */
 QVG_API qvg_status qvg_attention_weights(const qvg_config* cfg, const qvg_packed* k, int64_t Nk, int32_t H, int32_t d,
                                  const qvg_batch* batch, const void* tables, size_t tables_bytes,

@@ -395,6 +395,31 @@ def test_a_recorded_timeout_and_a_failed_launch_are_reported(q, ora, monkeypatch
     torch.cuda.synchronize()
 
 
+def test_weights_survive_a_recorded_timeout(q, ora):
+    """A captured call looks at no status word on the host.  Once an expired wait
+    is recorded its kernels leave the weights received before as they are, in
+    place or not; cleared, the next replay adds them again."""
+    for kw in (dict(H=2, Nq=300, Nk=3000), dict(H=1, Nq=1500, Nk=66, B=2, Nt=4)):       # the second: sums by key in cuts of the rows
+        case = Case(q, ora, seed=43, **kw)
+        received = torch.rand((case.H, case.Nk), generator=torch.Generator().manual_seed(4)).cuda()
+        want = q.attention_weights(case.kp, received=received, **case.args())
+        args, inplace, out, alone = case.args(), received.clone(), torch.full_like(received, 7.0), torch.full_like(received, 7.0)
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            q.attention_weights(case.kp, received=inplace, out=inplace, **args)
+            q.attention_weights(case.kp, received=received, out=out, **args)
+            q.attention_weights(case.kp, out=alone, **args)
+        case.tables[:4] = torch.tensor([1, 0, 0, 0], dtype=torch.uint8)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(inplace, received) and torch.equal(out, received) and torch.count_nonzero(alone) == 0
+        assert q.workspace_status(case.tables) == 5 and q.workspace_status(case.tables) == 0
+        gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(inplace, want) and torch.equal(out, want)
+        check_weights(case, alone)
+
+
 def test_packed_streams_on_another_device_are_refused(q, ora):
     import dataclasses
     case = Case(q, ora, seed=53, H=2, Nk=200, T=2)

@@ -320,6 +320,7 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
     }
     if (ok) {
       if (ntiles > 0) ok = bar_wait_or_abort(&sh->s_done[g], (uint32_t)(ntiles & 1), abort_flag);
+      __syncwarp();                                    // the lanes' waits end apart, the barrier below wants them together
       fence_after();
       // the two sums of a row joined, through the row tile, which no product reads any more
       float* sums = reinterpret_cast<float*>(sQ + g * kAtOpBytes);
@@ -338,9 +339,11 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           uint32_t rg[32];
+          __syncwarp();                                // a load of the whole warp, which the stores' branches divide
           tld32(tOt + 32 * c, rg);
-          if (row >= a.r1) continue;
-          if (whole) {
+          if (row >= a.r1) {
+            // behind the last row: nothing to store
+          } else if (whole) {
             uint4* dst = reinterpret_cast<uint4*>(p.O + query_row(p, a.h, row) * kD + 64 * side + 32 * c);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -367,6 +370,7 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, 1u);
   if (warp == 0) {
+    __syncwarp();
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }

@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
     // the row's or key's two halves joined, through the resident tile, which no
     // product reads any more
     float2* half = reinterpret_cast<float2*>(own + 2 * g * kAtOpBytes) + (threadIdx.x & 127);
+    __syncwarp();
     if (STATS) {
       if (side == 1) *half = make_float2(m_run, total);
       ok = !named_bar_or(1 + g, 256, !ok);
@@ -380,6 +381,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
   __syncthreads();
   if (threadIdx.x == 0 && *abort_flag) atomicOr(p.status, 1u);
   if (warp == 0) {
+    __syncwarp();
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }

@@ -310,6 +310,18 @@ def test_few_heads_are_cut_into_many_ranges(q, ora, kw):
     assert q.workspace_status(case.tables) == 0
 
 
+@pytest.mark.parametrize("kw", [
+    dict(H=12, Nk=100, Nq=1111),                                                  # one range: O by the CTA that has the rows
+    dict(H=12, Nk=100, Nq=1025, Nt=3),                                            # and a tail's: a single row in the last block
+    dict(H=1, Nk=12800, Nq=159, causal=True),                                     # cut into ranges, 31 rows behind a tile
+], ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items()))
+def test_last_warps_with_fewer_rows_than_lanes(q, ora, kw):
+    case = Case(q, ora, seed=59, T=2, **kw)
+    check_attention(case, q.attention_batch(case.kp, case.vp, **case.args()))
+    check_weights(case, q.attention_weights(case.kp, **case.args()))
+    assert q.workspace_status(case.tables) == 0
+
+
 def test_every_sequence_alone_gives_the_same(q, ora):
     """A batch of sequences gives each row what it gets alone, within the
     rounding of the weights against other running maxima."""

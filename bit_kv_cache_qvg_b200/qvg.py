@@ -6,7 +6,6 @@ missing, every call raises ``QvgError`` -- there is no fallback path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -183,14 +182,14 @@ def _torch_stream(stream, dev):
     return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
 
 
-_CURRENT = contextlib.nullcontext()
-
-
-def _memory(stream, dev):
-    """Memory for work on `stream` (None: the current one) comes from that stream's
-    own blocks: a block that the current stream has let go of may still be in use
-    by what is queued there, and nothing orders `stream` behind it."""
-    return _CURRENT if stream is None else torch.cuda.stream(_torch_stream(stream, dev))
+def _memory(stream, dev, make, *args, **kw):
+    """make(*args, **kw), memory for work on `stream` (None: the current one), from that
+    stream's own blocks: a block that the current stream has let go of may still be in
+    use by what is queued there, and nothing orders `stream` behind it."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(_torch_stream(stream, dev)):
+        return make(*args, **kw)
 
 
 def _returned(stream, dev, *tensors):
@@ -244,25 +243,29 @@ class Packed:
     def struct(self) -> _Packed:
         """The tensors' addresses (0 for an empty one).  The library takes them as
         contiguous arrays of these sizes: a tensor that is not one is refused."""
-        cfg, T, tokens = self.cfg, self.cfg.T, self.H * self.N
-        device, groups = self.codes.get_device(), tokens * (self.d // max(cfg.group_size, 1))
-        self._check("codes", self.codes, tokens * self.d // 4, device)
-        self._check("scale", self.scale, groups, device)
-        if cfg.scale_mode == ASYM:
-            self._check("zero", self.zero, groups, device)
-        if T > 0:
-            self._check("assign", self.assign, T * tokens, device)
-            self._check("centroids", self.centroids, T * self.H * cfg.K * self.d * (2 if self.dtype == BF16 else 4), device)
-        return self._addresses()
+        cfg, codes, scale, zero, assign, tables = self.cfg, self.codes, self.scale, self.zero, self.assign, self.centroids
+        T, d, tokens, device = cfg.T, self.d, self.H * self.N, codes.get_device()
+        groups = tokens * (d // (cfg.group_size or 1))
+        row = cfg.K * d * (2 if self.dtype == BF16 else 4)
+        if codes.nbytes * 4 != tokens * d or not codes.is_contiguous():
+            self._refuse("codes")
+        if scale.nbytes != groups or not scale.is_contiguous() or scale.get_device() != device:
+            self._refuse("scale")
+        if cfg.scale_mode == ASYM and (zero.nbytes != groups or not zero.is_contiguous() or zero.get_device() != device):
+            self._refuse("zero")
+        if T > 0 and (assign.nbytes != T * tokens or not assign.is_contiguous() or assign.get_device() != device):
+            self._refuse("assign")
+        if T > 0 and (tables.nbytes != T * self.H * row or not tables.is_contiguous() or tables.get_device() != device):
+            self._refuse("centroids")
+        return _Packed(codes.data_ptr(), scale.data_ptr(), zero.data_ptr(), assign.data_ptr(), tables.data_ptr())
+
+    def _refuse(self, name: str):
+        raise QvgError(1, f"{name} must be a contiguous tensor of the packed form's sizes, on the device of codes")
 
     def _addresses(self) -> _Packed:
+        """struct of tensors that were allocated for these sizes just now."""
         return _Packed(self.codes.data_ptr(), self.scale.data_ptr(), self.zero.data_ptr(), self.assign.data_ptr(),
                        self.centroids.data_ptr())
-
-    @staticmethod
-    def _check(name: str, t: torch.Tensor, size: int, device: int):
-        if t.nbytes != size or not t.is_contiguous() or t.get_device() != device:
-            raise QvgError(1, f"{name} must be a contiguous tensor of {size} bytes on the device of codes")
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in
@@ -300,8 +303,7 @@ def alloc_workspace(cfg: Config, N: int, H: int, d: int = 128, dtype: int = BF16
 
 def _new_packed(cfg: Config, N: int, H: int, d: int, dtype: int, dev, stream) -> Packed:
     """alloc_packed for the result of work on `stream`."""
-    with _memory(stream, dev):
-        p = alloc_packed(cfg, N, H, d, dtype, dev)
+    p = _memory(stream, dev, alloc_packed, cfg, N, H, d, dtype, dev)
     _returned(stream, dev, p.codes, p.scale, p.zero, p.assign, p.centroids)
     return p
 
@@ -317,8 +319,7 @@ def quantize(X: torch.Tensor, cfg: Config, init: Optional[torch.Tensor] = None,
     if out is None:
         out = _new_packed(cfg, N, H, d, dt, X.device, stream)
     if workspace is None:
-        with _memory(stream, X.device):
-            workspace = alloc_workspace(cfg, N, H, d, dt, X.device)
+        workspace = _memory(stream, X.device, alloc_workspace, cfg, N, H, d, dt, X.device)
     ps = out.struct()
     st = lib().qvg_quantize(C.byref(cfg), _ptr(X), dt, N, H, d, _ptr(init), C.byref(ps),
                             _ptr(workspace), workspace.numel(), _stream(stream))
@@ -344,8 +345,7 @@ def quantize_static(X: torch.Tensor, cfg: Config, init: Optional[torch.Tensor] =
 
 def dequantize(p: Packed, Y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     if Y is None:
-        with _memory(stream, p.codes.device):
-            Y = torch.empty((p.H, p.N, p.d), dtype=_TORCH[p.dtype], device=p.codes.device)
+        Y = _memory(stream, p.codes.device, torch.empty, (p.H, p.N, p.d), dtype=_TORCH[p.dtype], device=p.codes.device)
         _returned(stream, p.codes.device, Y)
     ps = p.struct()
     st = lib().qvg_dequantize(C.byref(p.cfg), C.byref(ps), p.dtype, p.N, p.H, p.d, _ptr(Y), _stream(stream))
@@ -360,8 +360,7 @@ def rope_tables(max_pos: int, base: float = 10000.0, d: int = 128, device="cuda"
     if n == 0:
         raise QvgError(1, "qvg_rope_tables_bytes")
     device = torch.device(device)
-    with _memory(stream, device):
-        t = torch.empty(n, dtype=torch.uint8, device=device)
+    t = _memory(stream, device, torch.empty, n, dtype=torch.uint8, device=device)
     _returned(stream, device, t)
     _check(lib().qvg_rope_tables(float(base), d, max_pos, _ptr(t), n, _stream(stream)), "qvg_rope_tables")
     return t
@@ -378,13 +377,11 @@ def attention(kp: Packed, vp: Packed, Q: torch.Tensor, q_pos: torch.Tensor, tabl
         raise QvgError(1, "Q must be a contiguous bf16 [H][Nq][d] tensor")
     H, Nq, d = Q.shape
     if O is None:
-        with _memory(stream, Q.device):
-            O = torch.empty((H, Nq, d), dtype=torch.float32, device=Q.device)
+        O = _memory(stream, Q.device, torch.empty, (H, Nq, d), dtype=torch.float32, device=Q.device)
         _returned(stream, Q.device, O)
     if workspace is True:
         n = attention_workspace_bytes(kp.cfg, kp.N, H, Nq)
-        with _memory(stream, Q.device):
-            workspace = torch.empty(n, dtype=torch.uint8, device=Q.device) if n > 0 else None
+        workspace = _memory(stream, Q.device, torch.empty, n, dtype=torch.uint8, device=Q.device) if n > 0 else None
     ws_ptr, ws_n = (_ptr(workspace), workspace.numel()) if workspace is not None else (None, 0)
     ks, vs = kp.struct(), vp.struct()
     _check(lib().qvg_attention(C.byref(kp.cfg), C.byref(ks), C.byref(vs), kp.N, H, d, _ptr(Q),
@@ -492,8 +489,7 @@ def _workspace(workspace, size_call, p: Packed, b: _Batch, dev, stream) -> torch
         else:
             with torch.cuda.device(dev):
                 need = size_call(C.byref(p.cfg), p.N, p.H, C.byref(b))
-        with _memory(stream, dev):
-            workspace = p.codes.new_empty(need)
+        workspace = _memory(stream, dev, p.codes.new_empty, need)
     elif workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or workspace.device != dev:
         raise QvgError(1, f"the workspace must be a contiguous uint8 tensor on {dev}")
     return workspace
@@ -522,8 +518,7 @@ def attention_batch(kp: Packed, vp: Packed, Q: torch.Tensor, q_pos: torch.Tensor
     L = lib()
     ws = _workspace(workspace, L.qvg_attention_batch_workspace_bytes, kp, b, dev, stream)
     if O is None:
-        with _memory(stream, dev):
-            O = torch.empty_like(Q)
+        O = _memory(stream, dev, torch.empty_like, Q)
         _returned(stream, dev, O)
     _check(_queue(dev, stream, L.qvg_attention_batch, C.byref(kp.cfg), C.byref(kp.struct()), C.byref(vp.struct()), kp.N, kp.H, kp.d,
                   C.byref(b), tables.data_ptr(), tables.numel(), O.data_ptr(), ws.data_ptr(), ws.numel()), "qvg_attention_batch")
@@ -546,8 +541,7 @@ def attention_weights(kp: Packed, Q: torch.Tensor, q_pos: torch.Tensor, tables: 
     L = lib()
     ws = _workspace(workspace, L.qvg_attention_weights_workspace_bytes, kp, b, dev, stream)
     if out is None:
-        with _memory(stream, dev):
-            out = torch.empty(shape, dtype=torch.float32, device=dev)
+        out = _memory(stream, dev, torch.empty, shape, dtype=torch.float32, device=dev)
         _returned(stream, dev, out)
     _check(_queue(dev, stream, L.qvg_attention_weights, C.byref(kp.cfg), C.byref(kp.struct()), kp.N, kp.H, kp.d, C.byref(b),
                   tables.data_ptr(), tables.numel(), before, out.data_ptr(), ws.data_ptr(), ws.numel()),
@@ -600,6 +594,11 @@ def _closed(kp: Packed, vp: Packed, keep: int):
     return out
 
 
+def _evicted(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int) -> Evicted:
+    shape, new = (kp.H, keep), weights.new_empty
+    return Evicted(*_closed(kp, vp, keep), new(shape, dtype=torch.int32), new(shape, dtype=torch.int64), new(shape))
+
+
 def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int = 0, recent: int = 0,
           k_pos: Optional[torch.Tensor] = None, stream=None) -> Evicted:
     """qvg_evict: keep the first `first` and the last `recent` tokens of every
@@ -613,11 +612,8 @@ def evict(kp: Packed, vp: Packed, weights: torch.Tensor, keep: int, first: int =
     at_pos = _device_tensor(k_pos, "k_pos", torch.int64, shape, dev)
     _on_device(kp.codes, vp.codes)
     ks, vs = kp.struct(), vp.struct()
-    shape = (kp.H, keep)
-    new = weights.new_empty
-    with _memory(stream, dev):
-        k, v = _closed(kp, vp, keep)
-        e = Evicted(k, v, new(shape, dtype=torch.int32), new(shape, dtype=torch.int64), new(shape))
+    e = _memory(stream, dev, _evicted, kp, vp, weights, keep)
+    k, v = e.k, e.v
     _returned(stream, dev, e.kept, e.pos, e.weights, k.codes)       # both caches' streams are one allocation
     _check(_queue(dev, stream, lib().qvg_evict, C.byref(kp.cfg), C.byref(ks), C.byref(vs), kp.N, kp.H, kp.d, at_w,
                   at_pos, keep, first, recent, C.byref(k._addresses()), C.byref(v._addresses()), e.kept.data_ptr(),
@@ -725,8 +721,7 @@ class Cache:
     def dequantize(self, Y: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         if Y is None:
             device = torch.device("cuda")
-            with _memory(stream, device):
-                Y = torch.empty((self.H, self.tokens, self.d), dtype=_TORCH[self.dtype], device=device)
+            Y = _memory(stream, device, torch.empty, (self.H, self.tokens, self.d), dtype=_TORCH[self.dtype], device=device)
             _returned(stream, device, Y)
         _check(lib().qvg_cache_dequantize(self._h, _ptr(Y), _stream(stream)), "qvg_cache_dequantize")
         return Y

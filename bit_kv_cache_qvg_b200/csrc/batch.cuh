@@ -39,17 +39,17 @@ struct BatchParams {
   // the prefix and S2 of every tail (0: another launch does).
   int S1, S2, slot2, slots;
   int64_t tiles1, tiles2;         // this launch's row tiles of a head, and of one sequence's rows
-  float* part_O;                  // [slots][H][R][d]: unnormalised O of each range
-  float2* part_ml;                // [slots][H][R]: (row maximum, row sum) of each range, base 2
+  float* part_O;                  // [slots][Hn][R][d]: unnormalised O of each range
+  float2* part_ml;                // [slots][Hn][R]: (row maximum, row sum) of each range, base 2
   __nv_bfloat16* O;               // where a single slot needs no merge
   int row_tiles;                  // tiles of 16 rows to a CTA of the kernels for few rows
   int row_cuts;                   // cuts of the rows for the sums by key (weights of many rows)
   float* part_w;                  // [row_cuts][Hn][Nkp]: their sums, when there are several
   float* scores;                  // [Hn][R][Nkp]: the prefix's scores, base 2 (weights of few rows)
   int64_t Nkp;                    // Nk padded to 64
-  // Tensor-core operands of heads h0 .. h0 + Hn - 1, laid out as the kernels'
-  // shared memory wants them (kernel_batch_expand.cu).
-  int h0, Hn;
+  int h0, Hn;                     // the launch's heads h0 .. h0 + Hn - 1: the workspace is theirs alone
+  // Tensor-core operands, laid out as the kernels' shared memory wants them
+  // (kernel_batch_expand.cu).
   int64_t nt1, nt2;               // tiles of 128 keys of the prefix and of a tail
   int64_t Rp, RBp;                // rows of a head, and of one sequence, padded to 256
   uint8_t* key_img[2];            // prefix, tails: [Hn][nt1], [B][Hn][nt2] tiles of 32 KB

@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(32 * rw_warps(MT, VALUES), rw_per_sm(MT, VALUE
         L += x.y * ex2(x.x - M);
       }
       const int r = a.r0 + 16 * mt + g + 8 * i;
-      if (r < a.r1 && !(VALUES && p.slots == 1)) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + r] = make_float2(M, L);
+      if (r < a.r1 && !(VALUES && p.slots == 1)) p.part_ml[((int64_t)a.slot * p.Hn + a.h - p.h0) * p.R + r] = make_float2(M, L);
     }
   }
   if (VALUES) {
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(32 * rw_warps(MT, VALUES), rw_per_sm(MT, VALUE
           for (int n = 0; n < kNt; ++n) row[4 * n] = pack2(o[t][n][2 * i] * inv, o[t][n][2 * i + 1] * inv);
           continue;
         }
-        float* row = p.part_O + (((int64_t)a.slot * p.H + a.h) * p.R + r) * kD + 8 * kNt * warp + 2 * c;
+        float* row = p.part_O + (((int64_t)a.slot * p.Hn + a.h - p.h0) * p.R + r) * kD + 8 * kNt * warp + 2 * c;
 #pragma unroll
         for (int n = 0; n < kNt; ++n) *reinterpret_cast<float2*>(row + 8 * n) = make_float2(o[t][n][2 * i], o[t][n][2 * i + 1]);
       }
@@ -412,14 +412,14 @@ __global__ void __launch_bounds__(32 * rw_warps(MT, VALUES), rw_per_sm(MT, VALUE
 __global__ void __launch_bounds__(128) qvg_weights_rows(const BatchParams p, const float* received, float* out) {
   extern __shared__ float lse[];
   const int per = (int)((p.Nk + 511) / 512), hl = (int)(blockIdx.x / per), h = p.h0 + hl;
-  const int64_t stride = (int64_t)p.H * p.R;
+  const int64_t stride = (int64_t)p.Hn * p.R;
   // as many lanes to a row (a power of two) as let all rows go at once, or two
   int per_row = 32;
   while (per_row > 2 && per_row * p.R > 128) per_row >>= 1;
   for (int r0 = 0; r0 < (int)p.R; r0 += 128 / per_row) {
     const int r = r0 + (int)threadIdx.x / per_row;
     float M = kNoMax, L = 0.0f;
-    const float2* ml = p.part_ml + (int64_t)h * p.R + min(r, (int)p.R - 1);
+    const float2* ml = p.part_ml + (int64_t)hl * p.R + min(r, (int)p.R - 1);
 #pragma unroll 1
     for (int s0 = (int)threadIdx.x % per_row; s0 < p.slots; s0 += 8 * per_row) {
       float2 x[8];
@@ -465,15 +465,15 @@ __global__ void __launch_bounds__(128) qvg_weights_rows(const BatchParams p, con
 // lane per four channels.
 __device__ __forceinline__ void store_joined(const BatchParams& p, int64_t row, const float4& acc, float L) {
   const float inv = L == 0.0f ? 0.0f : 1.0f / L;
-  const int h = (int)(row / p.R);
-  reinterpret_cast<uint2*>(p.O + query_row(p, h, row - (int64_t)h * p.R) * kD)[threadIdx.x & 31] =
+  const int hl = (int)(row / p.R);
+  reinterpret_cast<uint2*>(p.O + query_row(p, p.h0 + hl, row - (int64_t)hl * p.R) * kD)[threadIdx.x & 31] =
       make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
 }
 
 // Few ranges: a warp per row, with a running maximum.
 __global__ void __launch_bounds__(128) qvg_batch_merge(const BatchParams p) {
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), stride = p.R * p.H;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5), stride = p.R * p.Hn;
   if (row >= stride) return;
   float M = kNoMax, L = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(128) qvg_batch_merge_wide(const BatchParams p)
   __shared__ float4 acc_s[4][32];
   __shared__ float factor[kMaxSlots];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = blockIdx.x, stride = p.R * p.H;
+  const int64_t row = blockIdx.x, stride = p.R * p.Hn;
   constexpr int kPer = kMaxSlots / 32;
   float2 ml[kPer];
   float M = kNoMax, L = 0.0f;
@@ -595,7 +595,7 @@ cudaError_t launch_rows_weights(const BatchParams& p, const float* received, flo
 }
 
 cudaError_t launch_batch_merge(const BatchParams& p, cudaStream_t s) {
-  const int64_t rows = p.R * p.H;
+  const int64_t rows = p.R * p.Hn;
   if (p.slots > 8) qvg_batch_merge_wide<<<(unsigned)rows, 128, 0, s>>>(p);
   else qvg_batch_merge<<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p);
   return cudaGetLastError();

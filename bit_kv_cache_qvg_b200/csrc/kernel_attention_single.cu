@@ -263,7 +263,7 @@ __global__ void __launch_bounds__(kSgThreads, NR == 1 ? kSgPerSm : 4) qvg_attent
       p.O[query_row(p, a.h, a.r0 + r) * kD + threadIdx.x] = __float2bfloat16_rn(L == 0.0f ? 0.0f : O / L);
       continue;
     }
-    const int64_t out = ((int64_t)a.slot * p.H + a.h) * p.R + a.r0 + r;
+    const int64_t out = ((int64_t)a.slot * p.Hn + a.h - p.h0) * p.R + a.r0 + r;
     if (threadIdx.x == 0) p.part_ml[out] = make_float2(M, L);
     if (VALUES) p.part_O[out * kD + threadIdx.x] = O;
   }

@@ -69,7 +69,8 @@ constexpr uint32_t kIdescValues = kIdesc | (1u << 16);      // B N-major
 // What a CTA has to do.
 struct AdPlace {
   bool tail;
-  int hl, h, b, slot;
+  int hl, h, b;
+  uint32_t part;                  // place among the partial results: slot * Hn + hl
   int n;                          // keys of the prefix or tail (below 2^23)
   int j0, ntiles;                 // tiles of 128 keys
   int r0, r1;                     // rows of the head (below 2^23)
@@ -86,7 +87,7 @@ __device__ __forceinline__ AdPlace ad_place(const BatchParams& p) {
   a.h = p.h0 + a.hl;
   a.b = (int)(unit / (uint32_t)p.Hn);
   a.n = (int)(a.tail ? tail_length(p, a.b) : p.Nk);
-  a.slot = (int)(a.tail ? p.slot2 + range : range);
+  a.part = (a.tail ? (uint32_t)p.slot2 + range : range) * (uint32_t)p.Hn + (uint32_t)a.hl;
   a.r0 = (int)((a.tail ? a.b * p.RB : 0) + block * kAdRows);
   a.r1 = (int)(a.tail ? (a.b + 1) * p.RB : p.R);
   a.groups = a.r1 - a.r0 > kAtTile ? 2 : 1;
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(kAdThreads, 1) qvg_batch_attend(const BatchPar
     if (ok) {
       const bool whole = p.slots == 1;                 // nothing to join: O itself
       const bool dead = limit == kLimitNone || l_run == 0.0f;
-      const int64_t out = ((int64_t)a.slot * p.H + a.h) * p.R + row;
+      const int64_t out = (int64_t)a.part * p.R + row;
       if (row < a.r1 && side == 0 && !whole) p.part_ml[out] = make_float2(m_run, dead ? 0.0f : l_run);
       const float inv = dead ? 0.0f : 1.0f / l_run;
       if (ntiles > 0) {
@@ -468,7 +469,7 @@ size_t place(BatchParams& p, const BatchPlan& plan, bool values, char* ws) {
   };
   p.slots = plan.S1 + plan.S2;
   p.slot2 = plan.S1;
-  const size_t rows = (size_t)p.H * p.R;
+  const size_t rows = (size_t)plan.Hn * p.R;
   if (values) p.part_O = reinterpret_cast<float*>(take(p.slots > 1 ? p.slots * rows * kD * sizeof(float) : 0));
   p.part_ml = reinterpret_cast<float2*>(take(p.slots * rows * sizeof(float2)));
   if (!values && !plan.tc1) p.scores = reinterpret_cast<float*>(take((size_t)plan.Hn * p.R * p.Nkp * sizeof(float)));
@@ -530,13 +531,20 @@ void cut_few(int64_t u1, int64_t n1, int64_t u2, int64_t n2, int64_t room, doubl
 // The cut of the keys, by estimated times.  Many rows: a CTA holds an SM, its
 // start and end take 3 tiles, and a range's partial results cost their way
 // through memory (about a fifth of a tile per CTA's worth of rows and range).
-BatchPlan plan_batch(BatchParams& p, bool values) {
+//
+// `most` heads at a time at most; `images`
+// false: no operand tiles (attention only, the kernels for few rows take any).
+BatchPlan plan_heads(BatchParams& p, bool values, int64_t most, bool images) {
   BatchPlan plan{};
+  auto heads = [&](int64_t n) {
+    n = std::max<int64_t>(1, std::min<int64_t>(n, std::min<int64_t>(most, p.H)));
+    return (int)n;
+  };
   const double sms = (double)device_sm_count();
   const int64_t blocks = ((p.R + 63) / 64 * ((p.Nk + 63) / 64) + p.B * ((p.RB + 63) / 64) * ((p.Nt + 63) / 64)) * p.H;
-  plan.tc1 = p.R > kManyRows && !(values && blocks <= kFewBlocks);
+  plan.tc1 = p.R > kManyRows && !(values && (blocks <= kFewBlocks || !images));
   plan.tc2 = plan.tc1 && p.Nt > 0 && p.RB > kManyRows;
-  plan.Hn = p.H;
+  plan.Hn = heads(p.H);
   const int64_t few = plan.tc1 ? p.RB : p.R;       // rows of the CTAs of the kernels for few rows
   plan.row_tiles = few <= 16 ? 1 : few <= 32 ? 2 : 4;
   p.row_tiles = plan.row_tiles;
@@ -544,16 +552,18 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
   const int64_t tile = 16 * plan.row_tiles, step = plan.single ? kSingleStep : kRowStep;
   const int64_t room = (int64_t)sms * (plan.single ? single_per_sm(p, values) : rows_per_sm(p, values));
   const int64_t steps1 = plan.tc1 ? 0 : (p.Nk + step - 1) / step, steps2 = plan.tc2 ? 0 : (p.Nt + step - 1) / step;
-  if (!plan.tc1 && !values)
-    plan.Hn = (int)std::max<int64_t>(1, std::min<int64_t>(p.H, (int64_t)(kImageBudget / ((size_t)p.R * p.Nkp * sizeof(float)))));
+  if (plan.tc1) {
+    size_t per_head = (size_t)p.nt1 * 2 * kImageBytes;
+    if (plan.tc2) per_head += (size_t)p.B * p.nt2 * 2 * kImageBytes;
+    plan.Hn = heads((int64_t)(kImageBudget / per_head));
+  } else if (!values) {
+    plan.Hn = heads((int64_t)(kImageBudget / ((size_t)p.R * p.Nkp * sizeof(float))));
+  }
   if (steps1 + steps2 > 0) {
     const int64_t units1 = (p.R + tile - 1) / tile * plan.Hn, units2 = (p.RB + tile - 1) / tile * plan.Hn * p.B;
     cut_few(units1, steps1, units2, steps2, room, plan.single ? 6.0 : 1.5, &plan.S1, &plan.S2);
   }
   if (plan.tc1) {
-    size_t per_head = (size_t)p.nt1 * 2 * kImageBytes;
-    if (plan.tc2) per_head += (size_t)p.B * p.nt2 * 2 * kImageBytes;
-    plan.Hn = (int)std::max<int64_t>(1, std::min<int64_t>(p.H, (int64_t)(kImageBudget / per_head)));
     const int64_t u1 = (p.Rp / kAdRows) * plan.Hn, u2 = plan.tc2 ? (p.RBp / kAdRows) * plan.Hn * p.B : 0;
     double best = -1.0;
     for (int64_t s1 = 1; s1 <= std::min<int64_t>(p.nt1, kAdMaxRanges); ++s1) {
@@ -589,15 +599,33 @@ BatchPlan plan_batch(BatchParams& p, bool values) {
   return plan;
 }
 
+// The plan for a workspace of `room` bytes: where it does not hold what the
+// call would like, fewer heads at a time, and where not even one head's tiles
+// fit, attention without them.  One head's plan does not depend on how many there
+// are, so that what the call asks for with H = 1 is always enough.
+BatchPlan plan_within(BatchParams& p, bool values, size_t room) {
+  BatchPlan plan{};
+  for (const bool images : {true, false}) {
+    plan = plan_heads(p, values, p.H, images);
+    while (plan.bytes > room && plan.Hn > 1)
+      plan = plan_heads(p, values, std::min<int64_t>(plan.Hn - 1, (int64_t)((double)plan.Hn * ((double)room / (double)plan.bytes))), images);
+    if (plan.bytes <= room || !values || !plan.tc1) break;
+  }
+  return plan;
+}
+BatchPlan plan_batch(BatchParams& p, bool values) { return plan_heads(p, values, p.H, true); }
+
 // Partial results of few rows.
 cudaError_t launch_few(const BatchPlan& plan, const BatchParams& p, bool values, cudaStream_t s) {
   return plan.single ? launch_single_partial(p, values, s) : launch_rows_partial(p, values, s);
 }
 
 // The launch's share of the plan: what the kernels for few rows take, or the
-// tensor-core kernels.
-BatchParams share(const BatchParams& p, const BatchPlan& plan, bool tc) {
+// tensor-core kernels, of the heads from h0.
+BatchParams share(const BatchParams& p, const BatchPlan& plan, bool tc, int h0) {
   BatchParams q = p;
+  q.h0 = h0;
+  q.Hn = std::min(plan.Hn, p.H - h0);
   q.S1 = plan.tc1 == tc ? plan.S1 : 0;
   q.S2 = plan.tc2 == tc ? plan.S2 : 0;
   q.row_tiles = plan.row_tiles;
@@ -630,45 +658,38 @@ static cudaError_t queue_attention(const BatchPlan& plan, BatchParams& p, void* 
   place(p, plan, true, static_cast<char*>(ws));
   p.O = static_cast<__nv_bfloat16*>(O);
   cudaError_t e = cudaSuccess;
-  const BatchParams few = share(p, plan, false);
-  if (few.S1 + few.S2 > 0 && (e = launch_few(plan, few, true, s)) != cudaSuccess) return e;
-  if (plan.tc1) {
-    BatchParams q = share(p, plan, true);
-    for (q.h0 = 0; q.h0 < p.H; q.h0 += plan.Hn) {
-      q.Hn = std::min(plan.Hn, p.H - q.h0);
-      if ((e = launch_batch_expand(q, false, s)) != cudaSuccess) return e;
-      if ((e = launch_batch_attend(q, s)) != cudaSuccess) return e;
+  for (int h0 = 0; h0 < p.H; h0 += plan.Hn) {
+    const BatchParams few = share(p, plan, false, h0), tc = share(p, plan, true, h0);
+    if (few.S1 + few.S2 > 0 && (e = launch_few(plan, few, true, s)) != cudaSuccess) return e;
+    if (plan.tc1) {
+      if ((e = launch_batch_expand(tc, false, s)) != cudaSuccess) return e;
+      if ((e = launch_batch_attend(tc, s)) != cudaSuccess) return e;
     }
+    if (p.slots > 1 && (e = launch_batch_merge(few, s)) != cudaSuccess) return e;
   }
-  return p.slots == 1 ? e : launch_batch_merge(p, s);
+  return e;
 }
 
 static cudaError_t queue_weights(const BatchPlan& plan, BatchParams& p, const float* received, float* out, void* ws, cudaStream_t s) {
   place(p, plan, false, static_cast<char*>(ws));
   cudaError_t e = cudaSuccess;
-  BatchParams few = share(p, plan, false);
-  if (!plan.tc1) {
-    for (few.h0 = 0; few.h0 < p.H; few.h0 += plan.Hn) {
-      few.Hn = std::min(plan.Hn, p.H - few.h0);
-      if ((e = launch_few(plan, few, false, s)) != cudaSuccess) return e;
+  for (int h0 = 0; h0 < p.H; h0 += plan.Hn) {
+    const BatchParams few = share(p, plan, false, h0), tc = share(p, plan, true, h0);
+    if (few.S1 + few.S2 > 0 && (e = launch_few(plan, few, false, s)) != cudaSuccess) return e;
+    if (!plan.tc1) {
       if ((e = launch_rows_weights(few, received, out, s)) != cudaSuccess) return e;
+      continue;
     }
-    return e;
-  }
-  if (few.S2 > 0 && (e = launch_few(plan, few, false, s)) != cudaSuccess) return e;
-  BatchParams q = share(p, plan, true);
-  for (q.h0 = 0; q.h0 < p.H; q.h0 += plan.Hn) {
-    q.Hn = std::min(plan.Hn, p.H - q.h0);
-    if ((e = launch_batch_expand(q, true, s)) != cudaSuccess) return e;
-    if ((e = launch_batch_stats(q, s)) != cudaSuccess) return e;
-    if ((e = launch_batch_weights(q, p.lse, p.limits, received, out, s)) != cudaSuccess) return e;
+    if ((e = launch_batch_expand(tc, true, s)) != cudaSuccess) return e;
+    if ((e = launch_batch_stats(tc, s)) != cudaSuccess) return e;
+    if ((e = launch_batch_weights(tc, tc.lse, tc.limits, received, out, s)) != cudaSuccess) return e;
   }
   return e;
 }
 
 qvg_status launch_attention_batch(const BatchArgs& a, void* O, void* ws, size_t ws_bytes, cudaStream_t s) {
   BatchParams p = params_of(a);
-  const BatchPlan plan = plan_batch(p, true);
+  const BatchPlan plan = plan_within(p, true, ws_bytes);
   const qvg_status st = ready(plan, a, ws_bytes, s);
   if (st != QVG_OK) return st;
   return queue_attention(plan, p, O, ws, s) == cudaSuccess ? QVG_OK : QVG_ERR_CUDA;
@@ -676,7 +697,7 @@ qvg_status launch_attention_batch(const BatchArgs& a, void* O, void* ws, size_t 
 
 qvg_status launch_attention_weights(const BatchArgs& a, const float* received, float* out, void* ws, size_t ws_bytes, cudaStream_t s) {
   BatchParams p = params_of(a);
-  const BatchPlan plan = plan_batch(p, false);
+  const BatchPlan plan = plan_within(p, false, ws_bytes);
   const qvg_status st = ready(plan, a, ws_bytes, s);
   if (st != QVG_OK) return st;
   return queue_weights(plan, p, received, out, ws, s) == cudaSuccess ? QVG_OK : QVG_ERR_CUDA;

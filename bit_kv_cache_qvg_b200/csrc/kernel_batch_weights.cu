@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kWtThreads, 1) qvg_batch_weights(const BatchPa
     }
     if ((ok || !STATS) && in && side == 0) {
       if (STATS) {
-        if (p.slots > 1) p.part_ml[((int64_t)a.slot * p.H + a.h) * p.R + mine] = make_float2(m_run, limit == kLimitNone ? 0.0f : total);
+        if (p.slots > 1) p.part_ml[((int64_t)a.slot * p.Hn + a.hl) * p.R + mine] = make_float2(m_run, limit == kLimitNone ? 0.0f : total);
       } else if (p.row_cuts > 1) {
         p.part_w[((int64_t)a.slot * p.Hn + a.hl) * p.Nkp + mine] = total;
       } else {
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(256) qvg_batch_lse(const BatchParams p, float*
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (e >= p.Hn * p.Rp) return;
   const int hl = (int)(e / p.Rp);
-  const int64_t r = e - hl * p.Rp, row = (int64_t)(p.h0 + hl) * p.R + r, stride = (int64_t)p.H * p.R;
+  const int64_t r = e - hl * p.Rp, row = (int64_t)hl * p.R + r, stride = (int64_t)p.Hn * p.R;
   float x = INFINITY;
   int limit = kLimitAll;
   if (r < p.R) {

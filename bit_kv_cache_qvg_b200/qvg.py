@@ -509,7 +509,8 @@ def attention_batch(kp: Packed, vp: Packed, Q: torch.Tensor, q_pos: torch.Tensor
     Q [B][H * group][Nq][d] bf16 and q_pos [B][Nq] int64 (negative: a padding
     row); k_pos [H][N] int64, the cached tokens' positions (None: 0 .. N-1);
     returns O, like Q, zeros in rows that see no key.  `workspace`: a uint8
-    tensor of attention_batch_workspace_bytes (None: allocated here)."""
+    tensor of attention_batch_workspace_bytes (None: allocated here), or a smaller
+    one, down to what that gives for H = 1: fewer heads at a time."""
     dev = kp.codes.device
     b = _batch(kp, Q, q_pos, k_pos, tail, causal, True, dev)
     _same_kind(kp, vp)

@@ -382,8 +382,11 @@ typedef struct {
  *   tables  DEVICE rotary tables (qvg_rope_tables), 32-byte aligned
  *   O  DEVICE [B][H * group][Nq][d] bf16, 16-byte aligned
  *   workspace, ws_bytes  DEVICE scratch for the partial results of the ranges
- *      that the keys are cut into, 16-byte aligned, not shared with calls
- *      that may run at the same time (two captured graphs among them)
+ *      that the keys are cut into and, with many rows, for the rebuilt tokens, 16-byte
+ *      aligned, not shared with calls that may run at the same time (two
+ *      captured graphs among them).  Of
+ *      qvg_attention_batch_workspace_bytes, or smaller: then fewer heads go at a
+ *      time, down to what that function gives for the same batch with H = 1
  * Rotated queries and keys are rounded to fp16 for their products (magnitudes
  * beyond 65504 saturate) and the softmax weights to bf16, unless a head has one row,
  * where all is fp32; sums are fp32.
@@ -418,8 +421,10 @@ QVG_API qvg_status qvg_attention_weights(const qvg_config* cfg, const qvg_packed
                                  const float* received, float* out, void* workspace, size_t ws_bytes,
                                  qvg_stream_t stream);
 
-/* The workspace the two calls above need on the current device (its pointers
- * in `batch` are not read); 0 for invalid arguments or without a device. */
+/* The workspace the two calls above make use of on the current device (its
+ * pointers in `batch` are not read), up to about 1 GiB of rebuilt tokens or scores at a
+ * time; 0 for invalid arguments or without a device.  With H = 1: what a call
+ * of any number of heads gets by with. */
 QVG_API size_t qvg_attention_batch_workspace_bytes(const qvg_config* cfg, int64_t Nk, int32_t H,
                                            const qvg_batch* batch);
 QVG_API size_t qvg_attention_weights_workspace_bytes(const qvg_config* cfg, int64_t Nk, int32_t H,

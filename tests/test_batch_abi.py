@@ -95,6 +95,17 @@ def test_bad_arguments_are_refused(q):
     assert q.attention_weights_workspace_bytes(cfg, 10, 1, 0, 1, 1) == 0
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are not memory: without a device the launch fails instead")
+@pytest.mark.parametrize("b", [dict(B=4, Nq=380, Nt=380), dict(B=1, Nq=1560, Nt=0), dict(B=8, group=4, Nt=512), dict(B=16, group=4, Nt=0), dict(B=1, Nt=33)])
+def test_a_workspace_for_some_of_the_heads_is_enough(q, b):
+    """32 heads of 38,000 tokens ask for up to 1.3 GB; 64 MiB hold a few heads at a
+    time, 64 KiB not even one."""
+    cfg = q.config(K=256, T=2, group_size=64)
+    kw = dict(cfg=cfg, Nk=38000, H=32, positions=40000, b=batch(q, **b))
+    assert both(q, ws_bytes=64 << 20, **kw) == (4, 4)             # as far as the launch
+    assert both(q, ws_bytes=4096, **kw) == (6, 6)
+
+
 def evict(q, cfg=None, k=None, v=None, Nk=1000, H=4, d=128, weights=0x10000, k_pos=None, keep=500, first=4, recent=32, ko=None,
           vo=None, kept=0x20000, pos=0x30000, wout=0x40000):
     cfg = cfg or q.config(K=16, T=1, group_size=16)

@@ -322,6 +322,35 @@ def test_last_warps_with_fewer_rows_than_lanes(q, ora, kw):
     assert q.workspace_status(case.tables) == 0
 
 
+@pytest.mark.parametrize("kw", [
+    dict(Nk=2000, Nq=130, B=2, Nt=130, lens=[130, 77], T=2, K=64, causal=True, gaps=True),      # tiles of prefix and tails
+    dict(Nk=3200, Nq=20, B=4, group=2, Nt=40, lens=[40, 0, 7, 39], T=1),                        # tails of few rows
+    dict(Nk=6000, Nq=300, T=2),                                                                # one head alone has tiles, too
+    dict(Nk=90, Nq=900, B=2),                                                                  # sums by key in cuts of the rows
+    dict(Nk=3000, Nq=3, B=2, Nt=70, lens=[70, 1], T=3, G=8),
+    dict(Nk=3000, Nt=9, causal=True),
+], ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items() if k != "lens"))
+def test_smaller_workspaces_take_fewer_heads_at_a_time(q, ora, kw):
+    """From what a call asks for down to what it asks for with one head: the same
+    formula for every head, and not a byte behind the workspace is written."""
+    case = Case(q, ora, seed=61, H=5, **kw)
+    for call, size, check in (
+            (lambda ws: q.attention_batch(case.kp, case.vp, workspace=ws, **case.args()), q.attention_batch_workspace_bytes, check_attention),
+            (lambda ws: q.attention_weights(case.kp, workspace=ws, **case.args()), q.attention_weights_workspace_bytes, check_weights)):
+        full, least = (size(case.cfg, case.Nk, H, case.B, case.group, case.Nq, case.Nt) for H in (5, 1))
+        assert 0 < least <= full
+        for n in sorted({full, full - 1, full * 3 // 4, full // 2, full * 2 // 5, full // 4, least}, reverse=True):
+            n = max(n, least)
+            room = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+            out = call(room[:n])
+            assert torch.all(room[n:] == 0xA5)
+            check(case, out)
+        with pytest.raises(q.QvgError) as e:
+            call(torch.empty(16, dtype=torch.uint8, device="cuda"))
+        assert e.value.status == 6
+    assert q.workspace_status(case.tables) == 0
+
+
 def test_every_sequence_alone_gives_the_same(q, ora):
     """A batch of sequences gives each row what it gets alone, within the
     rounding of the weights against other running maxima."""

@@ -532,13 +532,15 @@ void cut_few(int64_t u1, int64_t n1, int64_t u2, int64_t n2, int64_t room, doubl
 // start and end take 3 tiles, and a range's partial results cost their way
 // through memory (about a fifth of a tile per CTA's worth of rows and range).
 //
-// `most` heads at a time at most; `images`
+// `most` heads at a time at most, in groups of about the same size (a last one of
+// few heads would leave SMs idle); `images`
 // false: no operand tiles (attention only, the kernels for few rows take any).
 BatchPlan plan_heads(BatchParams& p, bool values, int64_t most, bool images) {
   BatchPlan plan{};
   auto heads = [&](int64_t n) {
     n = std::max<int64_t>(1, std::min<int64_t>(n, std::min<int64_t>(most, p.H)));
-    return (int)n;
+    const int64_t groups = (p.H + n - 1) / n;
+    return (int)((p.H + groups - 1) / groups);
   };
   const double sms = (double)device_sm_count();
   const int64_t blocks = ((p.R + 63) / 64 * ((p.Nk + 63) / 64) + p.B * ((p.RB + 63) / 64) * ((p.Nt + 63) / 64)) * p.H;

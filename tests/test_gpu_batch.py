@@ -332,7 +332,8 @@ def test_last_warps_with_fewer_rows_than_lanes(q, ora, kw):
 ], ids=lambda kw: "-".join(f"{k}{v}" for k, v in kw.items() if k != "lens"))
 def test_smaller_workspaces_take_fewer_heads_at_a_time(q, ora, kw):
     """From what a call asks for down to what it asks for with one head: the same
-    formula for every head, and not a byte behind the workspace is written."""
+    formula for every head, and not a byte behind the workspace is written.  Five
+    heads go in groups of 5, of 3 and 2, of 2, 2 and 1, and one by one."""
     case = Case(q, ora, seed=61, H=5, **kw)
     for call, size, check in (
             (lambda ws: q.attention_batch(case.kp, case.vp, workspace=ws, **case.args()), q.attention_batch_workspace_bytes, check_attention),
@@ -349,6 +350,16 @@ def test_smaller_workspaces_take_fewer_heads_at_a_time(q, ora, kw):
             call(torch.empty(16, dtype=torch.uint8, device="cuda"))
         assert e.value.status == 6
     assert q.workspace_status(case.tables) == 0
+
+
+def test_heads_that_do_not_go_at_once_go_in_equal_groups(q):
+    """32 heads whose tiles or scores fit the workspace 29 or 31 at a time go as 16
+    and 16: what they ask for is what 16 heads do."""
+    cfg = q.config(K=256, T=2, group_size=64)
+    for size, Nk, rows in ((q.attention_batch_workspace_bytes, 66_000, 256), (q.attention_batch_workspace_bytes, 70_000, 1560),
+                           (q.attention_weights_workspace_bytes, 70_000, 1560), (q.attention_weights_workspace_bytes, 140_000, 64)):
+        two, one = (size(cfg, Nk, H, 1, 1, rows) for H in (32, 16))
+        assert 0 < two == one
 
 
 def test_every_sequence_alone_gives_the_same(q, ora):

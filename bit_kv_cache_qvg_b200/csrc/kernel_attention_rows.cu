@@ -92,7 +92,7 @@ __host__ __device__ constexpr int rw_per_sm(int mt, bool values) { return rw_war
 // unnormalised O, maximum and sum.  Without, the maximum and sum alone, and
 // the prefix's scores themselves (base 2, -inf where masked) to p.scores: each
 // from operands of two fp16 halves (three products: high x high, low x high,
-// high x low), so that they are good to fp32.
+// high x low), good to 2^-22, below 2^-3 to 2^-25 absolute.
 template <int TT, int MT, bool VALUES>
 __global__ void __launch_bounds__(32 * rw_warps(MT, VALUES), rw_per_sm(MT, VALUES)) qvg_attention_rows(const BatchParams p) {
   constexpr int W = rw_warps(MT, VALUES), kThreads = 32 * W;

@@ -9,9 +9,10 @@
 // M side of the product, so a key's sum stays in its threads and is taken
 // in one order, without atomics.
 //
-// A score must be good to fp32 (a sum of weights is an fp32 result), so each
-// operand is two fp16 halves and a score three products, high x high, low x
-// high and high x low: 24 tensor instructions a pair of tiles; the products are
+// A score must be good to about fp32 (a sum of weights is an fp32 result), so each
+// operand is two fp16 halves (2^-22 of itself, below 2^-3 2^-25 absolute) and a
+// score three products, high x high, low x high and high x low: 24 tensor
+// instructions a pair of tiles; the products are
 // the bound (12 heads, 1,560 rows, 24,960 keys: 311 and 300 us a pass, 1,180
 // TFLOP/s of products, 84 % of cuBLAS's sustained rate).
 // Stream tiles come as a high and a low half of 32 KB through a ring of three

@@ -387,9 +387,11 @@ typedef struct {
  *      captured graphs among them).  Of
  *      qvg_attention_batch_workspace_bytes, or smaller: then fewer heads go at a
  *      time, down to what that function gives for the same batch with H = 1
- * Rotated queries and keys are rounded to fp16 for their products (magnitudes
- * beyond 65504 saturate) and the softmax weights to bf16, unless a head has one row,
- * where all is fp32; sums are fp32.
+ * Rotated queries and keys are rounded to fp16 for their products (2^-11 relative,
+ * below 2^-14 2^-25 absolute; magnitudes beyond 65504 saturate, without an error) and
+ * the softmax weights to bf16; sums are fp32.  With one row a head all is fp32: the
+ * same sequence can then give other bits, and with magnitudes outside fp16's range
+ * another result, than beside a second one.
  * Errors: INVALID_ARG (also Nk < 1, Nq < 1, B < 1, group < 1, Nt < 0, or
  * tables that do not cover Nk - 1 when k_pos is NULL), UNSUPPORTED (d != 128,
  * B * group * Nq, H * B or Nt of 2^23 or more, B * group * Nq * H of 2^31 or
@@ -406,10 +408,12 @@ QVG_API qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* 
  * batch, added to what it received before:
  *   out[h][j] = received[h][j] + sum over the rows of head h of softmax(...)_j
  * with the softmax of qvg_attention_batch (over the prefix and the row's own
- * tail).  Products are taken from operands of 22 mantissa bits (the high and
- * low fp16 halves of rotated queries and keys; magnitudes beyond 65504
- * saturate) and every sum in fp32, in an order that does not depend on the
- * launch, so equal calls give equal bits.
+ * tail).  Products are taken from the high and low fp16 halves of rotated
+ * queries and keys: an operand is good to 2^-22 of itself down to 2^-3, and below to
+ * 2^-25 absolute (20 bits at 0.0123, 14 at 1e-4).  Beyond 65504 the halves keep 11
+ * bits and saturate.  With one or two rows a head the operands are fp32.  Every sum
+ * is taken in fp32, in an order that does not depend on the launch, so equal calls
+ * give equal bits.
  *   received  DEVICE [H][Nk] fp32, or NULL: zeros
  *   out       DEVICE [H][Nk] fp32; may be `received` itself.  After a recorded
  *             timeout (of this call or of earlier work) every token's out is its sum or

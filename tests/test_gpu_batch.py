@@ -296,6 +296,29 @@ def test_large_scores_and_far_positions(q, ora, Nq):
     check_weights(case, q.attention_weights(case.kp, **case.args()))
 
 
+@pytest.mark.parametrize("Nq", [1, 5, 400])
+def test_small_keys_and_large_queries(q, ora, Nq):
+    """Keys of a few thousandths and queries of some hundreds: the rounding of a
+    key's low half is absolute there."""
+    case = Case(q, ora, seed=67, Nk=900, Nq=Nq, B=2, T=1, K=64, mode=1, spread=2.0 ** -9, q_scale=300.0)
+    case.kp.scale.fill_(0x01)                           # 2^-9
+    case.Kh = rebuilt(ora, case.kp)
+    check_attention(case, q.attention_batch(case.kp, case.vp, **case.args()))
+    check_weights(case, q.attention_weights(case.kp, **case.args()))
+
+
+@pytest.mark.parametrize("Nq", [5, 400])
+def test_keys_beyond_fp16_saturate(q, ora, Nq, monkeypatch):
+    """A quarter of the keys' rotated channels beyond 65504: attention is that of the clipped ones."""
+    import sys
+    case = Case(q, ora, seed=71, Nk=900, Nq=Nq, B=2, T=1, K=64, mode=1, spread=6e4, q_scale=2e-5)
+    O = q.attention_batch(case.kp, case.vp, **case.args())
+    plain = rotated
+    assert 0.15 < (np.abs(plain(case.Kh[0], np.arange(case.Nk))) > 65504).mean() < 0.4
+    monkeypatch.setattr(sys.modules[__name__], "rotated", lambda x, pos: np.clip(plain(x, pos), -65504, 65504))
+    check_attention(case, O)
+
+
 @pytest.mark.parametrize("kw", [
     dict(H=1, Nk=20000),                                                          # as many ranges as one head is cut into
     dict(H=1, Nk=9000, Nq=3, Nt=9000, causal=True),                               # of the prefix and of the tail

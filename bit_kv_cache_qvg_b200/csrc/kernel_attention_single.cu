@@ -3,14 +3,16 @@
 //
 // With so few rows a tensor-core tile would be mostly padding, and the way there
 // (keys rounded to bf16, stored, read back as operands) costs more than the
-// products.  Here nothing leaves the registers: eight lanes take a key (two
+// products.  Here a key has no operand tile: eight lanes take it (two
 // 8-channel chunks each), rebuild and rotate it, multiply with the rotated
 // query and add up over the lanes; then they rebuild the value and add it,
 // weighted, to sums over the same 16 channels, all in fp32.  A warp works on four
 // keys at a time with a maximum and sum for each of its four groups of lanes, and meets
 // the others only at the end.  The tokens' bytes come 32 at a time through
 // shared memory (rebuild.cuh); loading them a block ahead cost registers, and
-// with them warps, worth more (six CTAs to an SM).  Bound by the instructions of
+// with them warps, worth more (six CTAs to an SM); at their 80
+// registers what a lane holds of a block's bytes between its loads and its stores
+// spills (192 bytes a thread with one stage, 256 with two, 544 with four).  Bound by the instructions of
 // the rebuilding and the latency of the centroid rows: 32 heads of 28,011 tokens
 // (K = 256, T = 1) take 142 us, 59 % of the issue slots and of the L1 data path;
 // one CTA of 24 warps, whose head's tables stay in the SM's L1, made it 158.

@@ -377,7 +377,9 @@ typedef struct {
  *   O[b][j][n] = softmax(rope(Q[b][j][n]) rope([K^[h]; tail_k[b][h]])^T / sqrt(d)) [V^[h]; tail_v[b][h]]
  * with h = j / group.  K^ and V^ are what qvg_dequantize would write for `k`
  * and `v` (two packed forms of H blocks of Nk tokens with the same cfg; bf16;
- * codes and centroids 16-byte aligned, scale and zero to d/G bytes).
+ * codes and centroids 16-byte aligned, scale and zero to d/G bytes).  Each is
+ * one packed form with one set of centroid tables: several chunks of a qvg_cache,
+ * which have a set each, are not.
  * A row that sees no key gets zeros.
  *   tables  DEVICE rotary tables (qvg_rope_tables), 32-byte aligned
  *   O  DEVICE [B][H * group][Nq][d] bf16, 16-byte aligned

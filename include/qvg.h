@@ -415,7 +415,7 @@ QVG_API qvg_status qvg_attention_batch(const qvg_config* cfg, const qvg_packed* 
  * 2^-25 absolute (20 bits at 0.0123, 14 at 1e-4).  Beyond 65504 the halves keep 11
  * bits and saturate.  With one or two rows a head the operands are fp32.  Every sum
  * is taken in fp32, in an order that does not depend on the launch, so equal calls
- * give equal bits.
+ * (with workspaces of one size) give equal bits.
  *   received  DEVICE [H][Nk] fp32, or NULL: zeros
  *   out       DEVICE [H][Nk] fp32; may be `received` itself.  After a recorded
  *             timeout (of this call or of earlier work) every token's out is its sum or
